@@ -13,6 +13,7 @@ HEADER = os.path.join(os.path.dirname(HERE), "include", "kla.h")
 _lib = None
 
 _vp, _i, _f, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
+_ll = ctypes.c_longlong
 
 SIGNATURES = {
     "kla_chunk_fwd_workspace_size": (_sz, [_i, _i, _i, _i, _i, _i]),
@@ -74,6 +75,20 @@ SIGNATURES = {
     "kla_gdn_chunk_bwd": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
                                _vp, _vp, _vp, _vp, _vp, _vp,
                                _i, _i, _i, _i, _i, _i, _vp, _sz, _vp]),
+    "kla_conv_fwd": (_i, [_vp, _ll] + 6 * [_vp] + 6 * [_i] + [_vp]),
+    "kla_conv_bwd_workspace_size": (_sz, 4 * [_i]),
+    "kla_conv_bwd": (_i, [_vp, _ll] + 10 * [_vp] + 6 * [_i] + [_vp, _sz, _vp]),
+    "kla_conv_step": (_i, [_vp, _ll] + 4 * [_vp] + 5 * [_i] + [_vp]),
+    "kla_ssm_fwd_workspace_size": (_sz, 5 * [_i]),
+    "kla_ssm_fwd": (_i, 12 * [_vp] + 5 * [_i] + 5 * [_ll] + 2 * [_i] + [_vp, _sz, _vp]),
+    "kla_ssm_bwd_workspace_size": (_sz, 5 * [_i]),
+    "kla_ssm_bwd": (_i, 21 * [_vp] + 5 * [_i] + 5 * [_ll] + 2 * [_i] + [_vp, _sz, _vp]),
+    "kla_ssm_step": (_i, 10 * [_vp] + 4 * [_i] + 5 * [_ll] + 2 * [_i] + [_vp]),
+    "kla_qk_norm_fwd": (_i, [_vp, _vp, _ll, _ll, _vp, _vp, _vp, _ll, _i, _vp, _i, _i, _f, _i,
+                             _f, _vp, _vp] + 6 * [_i] + [_vp]),
+    "kla_qk_norm_bwd_workspace_size": (_sz, 6 * [_i]),
+    "kla_qk_norm_bwd": (_i, [_vp, _vp, _ll, _ll, _vp, _vp, _vp, _ll, _i, _vp, _i, _i, _f, _i,
+                             _f] + 6 * [_vp] + 6 * [_i] + [_vp, _sz, _vp]),
     "kla_check_device_error": (_i, [_vp]),
     "kla_selftest_wait_timeout": (_i, [ctypes.c_uint, _vp]),
     "kla_status_string": (ctypes.c_char_p, [_i]),

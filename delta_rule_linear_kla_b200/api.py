@@ -594,6 +594,389 @@ def kda_decode_step_beta(q, k, v, g, beta, S, *, o=None, stream=None):
                        q, k, v, g, beta, None, S, o, stream)
 
 
+# ---------------------------------------------------------------------------
+# Layer operators around the recurrences: short causal convolution, selective
+# state space scan, norm and rotation of queries and keys.
+
+class _On:
+    """_on for calls of a few microseconds: no context is entered when the
+    tensors' device and its current stream are the ones to use anyway."""
+
+    __slots__ = ("dev", "stream", "ctx")
+
+    def __init__(self, ref, stream):
+        self.dev, self.stream, self.ctx = ref.device, stream, None
+
+    def __enter__(self):
+        if self.stream is None and torch.cuda.current_device() == self.dev.index:
+            return torch.cuda.current_stream(self.dev).cuda_stream
+        self.ctx = contextlib.ExitStack()
+        with contextlib.ExitStack() as stack:
+            stack.enter_context(torch.cuda.device(self.dev))
+            s = torch.cuda.current_stream(self.dev) if self.stream is None else self.stream
+            if s.device != self.dev:
+                raise ValueError("stream is on %s, the tensors on %s" % (s.device, self.dev))
+            stack.enter_context(torch.cuda.stream(s))
+            self.ctx = stack.pop_all()
+        return s.cuda_stream
+
+    def __exit__(self, *exc):
+        if self.ctx is not None:
+            self.ctx.close()
+
+
+def _rows(t, name, dtype, lead, inner, dev):
+    """Elements between the rows of an input that may be rows of a wider
+    matrix: shape lead + inner, inner contiguous, rows evenly spaced."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError("%s must be a CUDA tensor" % name)
+    if t.device != dev:
+        raise ValueError("%s is on %s, the call's other tensors on %s" % (name, t.device, dev))
+    if t.dtype != dtype:
+        raise ValueError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if t.shape != lead + inner:
+        raise ValueError("%s must have shape %s, got %s"
+                         % (name, tuple(lead + inner), tuple(t.shape)))
+    n = 1
+    for m in inner:
+        n *= m
+    if t.numel() == 0 or t.is_contiguous():
+        return n
+    st, want = t.stride(), 1
+    for i in range(len(t.shape) - 1, len(lead) - 1, -1):
+        if t.shape[i] != 1 and st[i] != want:
+            raise ValueError("%s: the elements of a row must be contiguous" % name)
+        want *= t.shape[i]
+    ld = None
+    span = 1
+    for i in range(len(lead) - 1, -1, -1):
+        if lead[i] != 1:
+            if ld is None:
+                ld = st[i] // span  # span is 1, or the rows before are single
+                if ld < n:
+                    raise ValueError("%s: rows must not overlap" % name)
+            if st[i] != ld * span:
+                raise ValueError("%s: rows must be evenly spaced" % name)
+        span *= lead[i]
+    return n if ld is None else ld
+
+
+def _act(t, name="x"):
+    """The activations' type of a call, from its first tensor."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype not in _DT:
+        raise ValueError("%s must be a CUDA tensor of dtype bfloat16 or float32" % name)
+    return t.dtype
+
+
+def _scratch(workspace, need, dev):
+    if workspace is None:
+        if need == 0:
+            return None, 0
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    _need(workspace, "workspace", torch.uint8, dev=dev)
+    return workspace, workspace.numel()
+
+
+def _dims(t, name, n):
+    if t.dim() != n:
+        raise ValueError("%s must have %d dimensions, got %s" % (name, n, tuple(t.shape)))
+    return tuple(t.shape)
+
+
+def conv_bwd_workspace_size(B: int, T: int, D: int, W: int) -> int:
+    return int(_native.lib().kla_conv_bwd_workspace_size(B, T, D, W))
+
+
+def _conv_args(x, w, bias, s0, lengths, lead):
+    dt, dev = x.dtype, x.device
+    D = x.shape[-1]
+    _need(w, "w", torch.float32, dev=dev)
+    if w is None or w.dim() != 2 or w.shape[0] != D:
+        raise ValueError("w must be a [D, W] CUDA tensor with D = %d" % D)
+    W = w.shape[1]
+    _need(bias, "bias", torch.float32, (D,), dev)
+    _need(s0, "s0", dt, (lead[0], W - 1, D), dev)
+    _need(lengths, "lengths", torch.int32, (lead[0],), dev)
+    return D, W, _rows(x, "x", dt, lead, (D,), dev)
+
+
+def conv_fwd(x, w, bias=None, s0=None, *, silu: bool = True, lengths=None, y=None, sT=None,
+             return_state: bool = True, stream=None):
+    """Short causal depthwise convolution of a prompt (kla_conv_fwd): x
+    [B,T,D] bf16 or fp32 (rows may be part of a wider matrix), w [D,W] fp32
+    with W in {2, 3, 4}, bias [D] fp32, s0 [B,W-1,D] the inputs before x,
+    lengths [B] int32.  Returns (y, sT), sT the last W-1 inputs."""
+    dt, dev = _act(x), x.device
+    B, T, _ = _dims(x, "x", 3)
+    with _On(x, stream) as s:
+        D, W, ldx = _conv_args(x, w, bias, s0, lengths, (B, T))
+        if y is None:
+            y = torch.empty((B, T, D), dtype=dt, device=dev)
+        _need(y, "y", dt, (B, T, D), dev)
+        if sT is None and return_state:
+            sT = torch.empty((B, W - 1, D), dtype=dt, device=dev)
+        _need(sT, "sT", dt, (B, W - 1, D), dev)
+        st = _native.lib().kla_conv_fwd(
+            _ptr(x), ldx, _ptr(w), _ptr(bias), _ptr(s0), _ptr(lengths), _ptr(y), _ptr(sT),
+            B, T, D, W, bool(silu), _DT[dt], s)
+    _check(st, "kla_conv_fwd")
+    return y, sT
+
+
+def conv_bwd(x, w, grad_y, bias=None, s0=None, grad_sT=None, *, silu: bool = True,
+             lengths=None, need_s0: bool = True, workspace=None, stream=None):
+    """Gradients of conv_fwd for dL/dy = grad_y and dL/dsT = grad_sT (None =
+    0) (kla_conv_bwd).  Returns a dict: dx and ds0 in x's type (ds0 None
+    unless need_s0), dw and dbias fp32 (dbias None without a bias)."""
+    dt, dev = _act(x), x.device
+    B, T, _ = _dims(x, "x", 3)
+    with _On(x, stream) as s:
+        D, W, ldx = _conv_args(x, w, bias, s0, lengths, (B, T))
+        _need_all(grad_y, "grad_y")
+        _need(grad_y, "grad_y", dt, (B, T, D), dev)
+        _need(grad_sT, "grad_sT", dt, (B, W - 1, D), dev)
+        f32 = dict(dtype=torch.float32, device=dev)
+        out = dict(dx=torch.empty((B, T, D), dtype=dt, device=dev),
+                   dw=torch.empty((D, W), **f32),
+                   dbias=None if bias is None else torch.empty((D,), **f32),
+                   ds0=torch.empty((B, W - 1, D), dtype=dt, device=dev) if need_s0 else None)
+        workspace, nws = _scratch(workspace, conv_bwd_workspace_size(B, T, D, W), dev)
+        st = _native.lib().kla_conv_bwd(
+            _ptr(x), ldx, _ptr(w), _ptr(bias), _ptr(s0), _ptr(lengths), _ptr(grad_y),
+            _ptr(grad_sT), _ptr(out["dx"]), _ptr(out["dw"]), _ptr(out["dbias"]),
+            _ptr(out["ds0"]), B, T, D, W, bool(silu), _DT[dt], _ptr(workspace), nws, s)
+    _check(st, "kla_conv_bwd")
+    return out
+
+
+def conv_step(x, w, state, bias=None, *, silu: bool = True, y=None, stream=None):
+    """One token of the convolution for each sequence (kla_conv_step): x
+    [B,D]; state [B,W-1,D] (conv_fwd's sT) is moved on in place.  Returns y
+    [B,D]."""
+    dt, dev = _act(x), x.device
+    B, _ = _dims(x, "x", 2)
+    with _On(x, stream) as s:
+        _need_all(state, "state")
+        D, W, ldx = _conv_args(x, w, bias, state, None, (B,))
+        if y is None:
+            y = torch.empty((B, D), dtype=dt, device=dev)
+        _need(y, "y", dt, (B, D), dev)
+        st = _native.lib().kla_conv_step(
+            _ptr(x), ldx, _ptr(w), _ptr(bias), _ptr(state), _ptr(y), B, D, W, bool(silu),
+            _DT[dt], s)
+    _check(st, "kla_conv_step")
+    return y
+
+
+def _need_all(t, name):
+    if t is None:
+        raise ValueError("%s must be a CUDA tensor" % name)
+
+
+def ssm_fwd_workspace_size(B: int, T: int, D: int, G: int, N: int) -> int:
+    return int(_native.lib().kla_ssm_fwd_workspace_size(B, T, D, G, N))
+
+
+def ssm_bwd_workspace_size(B: int, T: int, D: int, G: int, N: int) -> int:
+    return int(_native.lib().kla_ssm_bwd_workspace_size(B, T, D, G, N))
+
+
+def _ssm_args(u, dt, A, Bm, Cm, D, z, dt_bias, lead):
+    """Checks the inputs that prompts and single tokens share; returns the
+    sizes and the row pitches of u, dt, Bm, Cm and z."""
+    ty, dev = u.dtype, u.device
+    Dn = u.shape[-1]
+    _need_all(A, "A")
+    _need(A, "A", torch.float32, dev=dev)
+    if A.dim() != 2 or A.shape[0] != Dn:
+        raise ValueError("A must be [D, N] with D = %d, got %s" % (Dn, tuple(A.shape)))
+    N = A.shape[1]
+    _need_all(Bm, "Bm")
+    if not isinstance(Bm, torch.Tensor) or Bm.dim() != len(lead) + 2:
+        raise ValueError("Bm must be a CUDA tensor of shape [..., G, N]")
+    G = Bm.shape[-2]
+    _need(D, "D", torch.float32, (Dn,), dev)
+    _need(dt_bias, "dt_bias", torch.float32, (Dn,), dev)
+    lds = (_rows(u, "u", ty, lead, (Dn,), dev), _rows(dt, "dt", ty, lead, (Dn,), dev),
+           _rows(Bm, "Bm", ty, lead, (G, N), dev), _rows(Cm, "Cm", ty, lead, (G, N), dev),
+           0 if z is None else _rows(z, "z", ty, lead, (Dn,), dev))
+    return Dn, G, N, lds
+
+
+def ssm_fwd(u, dt, A, Bm, Cm, D=None, z=None, dt_bias=None, h0=None, *, softplus: bool = True,
+            lengths=None, y=None, hT=None, return_state: bool = True, workspace=None,
+            stream=None):
+    """Selective state space scan of a prompt (kla_ssm_fwd): u, dt, z
+    [B,T,D], Bm, Cm [B,T,G,N] bf16 or fp32 (rows may be parts of wider
+    matrices), A [D,N], D, dt_bias [D], h0 [B,D,N] fp32, lengths [B] int32;
+    N in {8, 16, 32, 64}.  Returns (y, hT)."""
+    ty, dev = _act(u, "u"), u.device
+    B, T, _ = _dims(u, "u", 3)
+    with _On(u, stream) as s:
+        Dn, G, N, lds = _ssm_args(u, dt, A, Bm, Cm, D, z, dt_bias, (B, T))
+        _need(h0, "h0", torch.float32, (B, Dn, N), dev)
+        _need(lengths, "lengths", torch.int32, (B,), dev)
+        if y is None:
+            y = torch.empty((B, T, Dn), dtype=ty, device=dev)
+        _need(y, "y", ty, (B, T, Dn), dev)
+        if hT is None and return_state:
+            hT = torch.empty((B, Dn, N), dtype=torch.float32, device=dev)
+        _need(hT, "hT", torch.float32, (B, Dn, N), dev)
+        workspace, nws = _scratch(workspace, ssm_fwd_workspace_size(B, T, Dn, G, N), dev)
+        st = _native.lib().kla_ssm_fwd(
+            _ptr(u), _ptr(dt), _ptr(A), _ptr(Bm), _ptr(Cm), _ptr(D), _ptr(z), _ptr(dt_bias),
+            _ptr(h0), _ptr(lengths), _ptr(y), _ptr(hT), B, T, Dn, G, N, *lds, bool(softplus),
+            _DT[ty], _ptr(workspace), nws, s)
+    _check(st, "kla_ssm_fwd")
+    return y, hT
+
+
+def ssm_bwd(u, dt, A, Bm, Cm, grad_y, D=None, z=None, dt_bias=None, h0=None, grad_hT=None, *,
+            softplus: bool = True, lengths=None, need_h0: bool = True, workspace=None,
+            stream=None):
+    """Gradients of ssm_fwd for dL/dy = grad_y and dL/dhT = grad_hT (None =
+    0) (kla_ssm_bwd).  Returns a dict: du, ddt, dB, dC, dz in u's type, dA,
+    dD, ddt_bias, dh0 fp32 (None for inputs that are None; dh0 None unless
+    need_h0)."""
+    ty, dev = _act(u, "u"), u.device
+    B, T, _ = _dims(u, "u", 3)
+    with _On(u, stream) as s:
+        Dn, G, N, lds = _ssm_args(u, dt, A, Bm, Cm, D, z, dt_bias, (B, T))
+        _need(h0, "h0", torch.float32, (B, Dn, N), dev)
+        _need(lengths, "lengths", torch.int32, (B,), dev)
+        _need_all(grad_y, "grad_y")
+        _need(grad_y, "grad_y", ty, (B, T, Dn), dev)
+        _need(grad_hT, "grad_hT", torch.float32, (B, Dn, N), dev)
+        act = dict(dtype=ty, device=dev)
+        f32 = dict(dtype=torch.float32, device=dev)
+        out = dict(du=torch.empty((B, T, Dn), **act), ddt=torch.empty((B, T, Dn), **act),
+                   dA=torch.empty((Dn, N), **f32), dB=torch.empty((B, T, G, N), **act),
+                   dC=torch.empty((B, T, G, N), **act),
+                   dD=None if D is None else torch.empty((Dn,), **f32),
+                   dz=None if z is None else torch.empty((B, T, Dn), **act),
+                   ddt_bias=None if dt_bias is None else torch.empty((Dn,), **f32),
+                   dh0=torch.empty((B, Dn, N), **f32) if need_h0 else None)
+        workspace, nws = _scratch(workspace, ssm_bwd_workspace_size(B, T, Dn, G, N), dev)
+        st = _native.lib().kla_ssm_bwd(
+            _ptr(u), _ptr(dt), _ptr(A), _ptr(Bm), _ptr(Cm), _ptr(D), _ptr(z), _ptr(dt_bias),
+            _ptr(h0), _ptr(lengths), _ptr(grad_y), _ptr(grad_hT), _ptr(out["du"]),
+            _ptr(out["ddt"]), _ptr(out["dA"]), _ptr(out["dB"]), _ptr(out["dC"]),
+            _ptr(out["dD"]), _ptr(out["dz"]), _ptr(out["ddt_bias"]), _ptr(out["dh0"]), B, T, Dn,
+            G, N, *lds, bool(softplus), _DT[ty], _ptr(workspace), nws, s)
+    _check(st, "kla_ssm_bwd")
+    return out
+
+
+def ssm_step(u, dt, A, Bm, Cm, state, D=None, z=None, dt_bias=None, *, softplus: bool = True,
+             y=None, stream=None):
+    """One token of the scan for each sequence (kla_ssm_step): u, dt, z
+    [B,D], Bm, Cm [B,G,N]; state [B,D,N] fp32 (ssm_fwd's hT) is moved on in
+    place.  Returns y [B,D]."""
+    ty, dev = _act(u, "u"), u.device
+    B, _ = _dims(u, "u", 2)
+    with _On(u, stream) as s:
+        Dn, G, N, lds = _ssm_args(u, dt, A, Bm, Cm, D, z, dt_bias, (B,))
+        _need_all(state, "state")
+        _need(state, "state", torch.float32, (B, Dn, N), dev)
+        if y is None:
+            y = torch.empty((B, Dn), dtype=ty, device=dev)
+        _need(y, "y", ty, (B, Dn), dev)
+        st = _native.lib().kla_ssm_step(
+            _ptr(u), _ptr(dt), _ptr(A), _ptr(Bm), _ptr(Cm), _ptr(D), _ptr(z), _ptr(dt_bias),
+            _ptr(state), _ptr(y), B, Dn, G, N, *lds, bool(softplus), _DT[ty], s)
+    _check(st, "kla_ssm_step")
+    return y
+
+
+_NORMS = {None: 0, "l2": 1, "rms": 2}
+
+
+def _qk_args(q, k, wq, wk, positions, inv_freq, norm):
+    ty, dev = q.dtype, q.device
+    one = q.dim() == 3  # a single token of each sequence: [B, H, d]
+    lead = (q.shape[0],) if one else tuple(q.shape[:2])
+    if q.dim() not in (3, 4) or not isinstance(k, torch.Tensor) or k.dim() != q.dim():
+        raise ValueError("q and k must be CUDA tensors [B, T, H, d] or [B, H, d]")
+    B, T = lead[0], 1 if one else lead[1]
+    Hq, d = q.shape[-2:]
+    Hk = k.shape[-2]
+    ldq, ldk = _rows(q, "q", ty, lead, (Hq, d), dev), _rows(k, "k", ty, lead, (Hk, d), dev)
+    _need(wq, "wq", torch.float32, (d,), dev)
+    _need(wk, "wk", torch.float32, (d,), dev)
+    _need(inv_freq, "inv_freq", torch.float32, dev=dev)
+    if norm not in _NORMS:
+        raise ValueError("norm must be None, 'l2' or 'rms', got %r" % (norm,))
+    stride = 0
+    if positions is not None:
+        _need(positions, "positions", torch.int32, dev=dev)
+        shape = tuple(positions.shape)
+        if shape == (lead if one else (B, T)):
+            stride = T
+        elif one or shape != (T,):
+            raise ValueError("positions must have shape %s, got %s"
+                             % (lead if one else "%s or %s" % ((B, T), (T,)), shape))
+    rot = 0 if inv_freq is None else 2 * inv_freq.numel()
+    return B, T, Hq, Hk, d, ldq, ldk, stride, rot
+
+
+def qk_norm_bwd_workspace_size(B: int, T: int, Hq: int, Hk: int, d: int, rot: int) -> int:
+    return int(_native.lib().kla_qk_norm_bwd_workspace_size(B, T, Hq, Hk, d, rot))
+
+
+def qk_norm_fwd(q, k, *, wq=None, wk=None, positions=None, inv_freq=None, pos0: int = 0,
+                norm: Optional[str] = "l2", eps: float = 1e-6, interleaved: bool = False,
+                scale: float = 1.0, oq=None, ok=None, stream=None):
+    """Norm of every head of q [B,T,Hq,d] and k [B,T,Hk,d] (or [B,H,d], one
+    token of each sequence) and rotation of its first 2 * len(inv_freq)
+    channels by position, in one pass (kla_qk_norm_fwd).  norm: "l2", "rms"
+    or None; wq, wk [d] fp32; positions int32 [B,T], [T] or (one token) [B],
+    None = pos0 + t; inv_freq fp32, None = no rotation.  Returns (oq, ok)."""
+    ty, dev = _act(q, "q"), q.device
+    with _On(q, stream) as s:
+        B, T, Hq, Hk, d, ldq, ldk, ps, rot = _qk_args(q, k, wq, wk, positions, inv_freq, norm)
+        if oq is None:
+            oq = torch.empty(q.shape, dtype=ty, device=dev)
+        if ok is None:
+            ok = torch.empty(k.shape, dtype=ty, device=dev)
+        _need(oq, "oq", ty, q.shape, dev)
+        _need(ok, "ok", ty, k.shape, dev)
+        st = _native.lib().kla_qk_norm_fwd(
+            _ptr(q), _ptr(k), ldq, ldk, _ptr(wq), _ptr(wk), _ptr(positions), ps, pos0,
+            _ptr(inv_freq), rot, bool(interleaved), float(scale), _NORMS[norm], float(eps),
+            _ptr(oq), _ptr(ok), B, T, Hq, Hk, d, _DT[ty], s)
+    _check(st, "kla_qk_norm_fwd")
+    return oq, ok
+
+
+def qk_norm_bwd(q, k, grad_oq, grad_ok, *, wq=None, wk=None, positions=None, inv_freq=None,
+                pos0: int = 0, norm: Optional[str] = "l2", eps: float = 1e-6,
+                interleaved: bool = False, scale: float = 1.0, workspace=None, stream=None):
+    """Gradients of qk_norm_fwd (kla_qk_norm_bwd).  Returns a dict: dq, dk in
+    q's type, dwq, dwk fp32 (None for weights that are None)."""
+    ty, dev = _act(q, "q"), q.device
+    with _On(q, stream) as s:
+        B, T, Hq, Hk, d, ldq, ldk, ps, rot = _qk_args(q, k, wq, wk, positions, inv_freq, norm)
+        _need_all(grad_oq, "grad_oq")
+        _need_all(grad_ok, "grad_ok")
+        _need(grad_oq, "grad_oq", ty, q.shape, dev)
+        _need(grad_ok, "grad_ok", ty, k.shape, dev)
+        out = dict(dq=torch.empty(q.shape, dtype=ty, device=dev),
+                   dk=torch.empty(k.shape, dtype=ty, device=dev),
+                   dwq=None if wq is None else torch.empty_like(wq),
+                   dwk=None if wk is None else torch.empty_like(wk))
+        need = 0
+        if wq is not None or wk is not None:
+            need = qk_norm_bwd_workspace_size(B, T, Hq, Hk, d, rot)
+        workspace, nws = _scratch(workspace, need, dev)
+        st = _native.lib().kla_qk_norm_bwd(
+            _ptr(q), _ptr(k), ldq, ldk, _ptr(wq), _ptr(wk), _ptr(positions), ps, pos0,
+            _ptr(inv_freq), rot, bool(interleaved), float(scale), _NORMS[norm], float(eps),
+            _ptr(grad_oq), _ptr(grad_ok), _ptr(out["dq"]), _ptr(out["dk"]), _ptr(out["dwq"]),
+            _ptr(out["dwk"]), B, T, Hq, Hk, d, _DT[ty], _ptr(workspace), nws, s)
+    _check(st, "kla_qk_norm_bwd")
+    return out
+
+
 def check_device_error(stream=None):
     """Synchronise and raise KLAError if a kernel reported a timed-out wait
     (on the device of ``stream``; default: the current device's current

@@ -1,0 +1,599 @@
+// Short causal depthwise convolution: the mixing of neighbouring tokens in
+// front of a linear-attention recurrence, for prompts, their backward pass
+// and single tokens.
+//
+//   p[t][d] = bias[d] + sum_{j<W} w[d][j] x[t-W+1+j][d],   y = p or p sigmoid(p)
+//
+// with x[-W+1 .. -1] the state s0 (the last W-1 inputs of what came before).
+// All arithmetic is fp32; only y (and dx, ds0) are rounded, once, to the
+// activations' type.
+#include "kla_layer.cuh"
+
+namespace kla {
+namespace conv {
+
+using namespace layer;
+
+// Eight (bf16) or four (fp32) channels at a time where rows allow 16-byte
+// accesses, one channel otherwise.
+template <typename T, int V>
+struct Row;
+template <>
+struct Row<__nv_bfloat16, 8> {
+  uint4 r;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) {
+    r = *reinterpret_cast<const uint4*>(p);
+  }
+  __device__ __forceinline__ void zero() { r = make_uint4(0, 0, 0, 0); }
+  __device__ __forceinline__ void get(float (&f)[8]) const {
+    const uint32_t u[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f[2 * i] = __uint_as_float(u[i] << 16);
+      f[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+    }
+  }
+  __device__ __forceinline__ void set(const float (&f)[8]) {
+    uint32_t u[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+      u[i] = *reinterpret_cast<uint32_t*>(&h);
+    }
+    r = make_uint4(u[0], u[1], u[2], u[3]);
+  }
+  __device__ __forceinline__ void store(__nv_bfloat16* p) const {
+    *reinterpret_cast<uint4*>(p) = r;
+  }
+};
+template <>
+struct Row<__nv_bfloat16, 4> {
+  uint2 r;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) {
+    r = *reinterpret_cast<const uint2*>(p);
+  }
+  __device__ __forceinline__ void zero() { r = make_uint2(0, 0); }
+  __device__ __forceinline__ void get(float (&f)[4]) const {
+    f[0] = __uint_as_float(r.x << 16);
+    f[1] = __uint_as_float(r.x & 0xffff0000u);
+    f[2] = __uint_as_float(r.y << 16);
+    f[3] = __uint_as_float(r.y & 0xffff0000u);
+  }
+  __device__ __forceinline__ void set(const float (&f)[4]) {
+    __nv_bfloat162 a = __floats2bfloat162_rn(f[0], f[1]), b = __floats2bfloat162_rn(f[2], f[3]);
+    r = make_uint2(*reinterpret_cast<uint32_t*>(&a), *reinterpret_cast<uint32_t*>(&b));
+  }
+  __device__ __forceinline__ void store(__nv_bfloat16* p) const {
+    *reinterpret_cast<uint2*>(p) = r;
+  }
+};
+template <>
+struct Row<float, 4> {
+  float4 r;
+  __device__ __forceinline__ void load(const float* p) {
+    r = *reinterpret_cast<const float4*>(p);
+  }
+  __device__ __forceinline__ void zero() { r = make_float4(0.f, 0.f, 0.f, 0.f); }
+  __device__ __forceinline__ void get(float (&f)[4]) const {
+    f[0] = r.x; f[1] = r.y; f[2] = r.z; f[3] = r.w;
+  }
+  __device__ __forceinline__ void set(const float (&f)[4]) {
+    r = make_float4(f[0], f[1], f[2], f[3]);
+  }
+  __device__ __forceinline__ void store(float* p) const { *reinterpret_cast<float4*>(p) = r; }
+};
+template <typename T>
+struct Row<T, 1> {
+  T r;
+  __device__ __forceinline__ void load(const T* p) { r = *p; }
+  __device__ __forceinline__ void zero() { IO<T>::st(&r, 0.f); }
+  __device__ __forceinline__ void get(float (&f)[1]) const { f[0] = IO<T>::ld(&r); }
+  __device__ __forceinline__ void set(const float (&f)[1]) { IO<T>::st(&r, f[0]); }
+  __device__ __forceinline__ void store(T* p) const { *p = r; }
+};
+
+// Row i of a sequence's inputs, i in [-(W-1), T): the state before 0.
+template <typename T, int V, int W>
+__device__ __forceinline__ Row<T, V> input_row(const T* xb, long long ldx, const T* s0b, int D,
+                                               int i) {
+  Row<T, V> r;
+  if (i >= 0)
+    r.load(xb + (long long)i * ldx);
+  else if (s0b)
+    r.load(s0b + (long long)(W - 1 + i) * D);
+  else
+    r.zero();
+  return r;
+}
+
+template <int V, int W>
+__device__ __forceinline__ void load_taps(const float* w, const float* bias, int c,
+                                          float (&tap)[W][V], float (&b0)[V]) {
+#pragma unroll
+  for (int e = 0; e < V; ++e) {
+#pragma unroll
+    for (int j = 0; j < W; ++j) tap[j][e] = w[(long long)(c + e) * W + j];
+    b0[e] = bias ? bias[c + e] : 0.f;
+  }
+}
+
+// ---------------------------------------------------------------- prompt
+//
+// Bound by HBM: one read of x and one write of y.  A thread walks L tokens of
+// V channels with the last W-1 inputs in registers, so that x is read once
+// but for W-1 rows at the start of each walk (from L2); neighbouring lanes
+// hold neighbouring channels.  Four rows are loaded before the first is used.
+template <typename T, int V, int W, bool SILU>
+__global__ void __launch_bounds__(256)
+conv_fwd_kernel(const T* __restrict__ x, long long ldx, const float* __restrict__ w,
+                const float* __restrict__ bias, const T* __restrict__ s0,
+                const int* __restrict__ lengths, T* __restrict__ y, T* __restrict__ sT,
+                int Tn, int D, int CG, int NB, int L, long long total) {
+  const long long id = (long long)blockIdx.x * 256 + threadIdx.x;
+  if (id >= total) return;
+  const int cg = (int)(id % CG);
+  const long long rest = id / CG;
+  const int tb = (int)(rest % NB), b = (int)(rest / NB);
+  const int c = cg * V;
+  const int n = live_tokens(lengths, b, Tn);
+  const T* xb = x + (long long)b * Tn * ldx + c;
+  const T* s0b = s0 ? s0 + (long long)b * (W - 1) * D + c : nullptr;
+  T* yb = y + (long long)b * Tn * D + c;
+
+  float tap[W][V], b0[V];
+  load_taps<V, W>(w, bias, c, tap, b0);
+
+  const int t0 = tb * L, t1 = min(Tn, t0 + L), tn = min(t1, n);
+  float win[W - 1][V];  // win[j] = row t - (W-1) + j
+  if (t0 < tn) {
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j)
+      input_row<T, V, W>(xb, ldx, s0b, D, t0 - (W - 1) + j).get(win[j]);
+  }
+  auto one = [&](const Row<T, V>& r, int t) {
+    float cur[V], out[V];
+    r.get(cur);
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+      float p = b0[e];
+#pragma unroll
+      for (int j = 0; j < W - 1; ++j) p = fmaf(tap[j][e], win[j][e], p);
+      p = fmaf(tap[W - 1][e], cur[e], p);
+      out[e] = SILU ? silu(p) : p;
+#pragma unroll
+      for (int j = 0; j + 1 < W - 1; ++j) win[j][e] = win[j + 1][e];
+      win[W - 2][e] = cur[e];
+    }
+    Row<T, V> o;
+    o.set(out);
+    o.store(yb + (long long)t * D);
+  };
+  int t = t0;
+  for (; t + 4 <= tn; t += 4) {
+    Row<T, V> r[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r[i].load(xb + (long long)(t + i) * ldx);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) one(r[i], t + i);
+  }
+  for (; t < tn; ++t) {
+    Row<T, V> r;
+    r.load(xb + (long long)t * ldx);
+    one(r, t);
+  }
+  Row<T, V> zero;
+  zero.zero();
+  for (t = max(t0, tn); t < t1; ++t) zero.store(yb + (long long)t * D);
+
+  if (sT && tb == NB - 1) {  // the last W-1 inputs that exist
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j)
+      input_row<T, V, W>(xb, ldx, s0b, D, n - (W - 1) + j)
+          .store(sT + ((long long)b * (W - 1) + j) * D + c);
+  }
+}
+
+// ---------------------------------------------------------------- backward
+//
+// dp = dy act'(p);  dx[i] = sum_j w[j] dp[i + W-1-j];  dw[j] = sum_t dp[t]
+// x[t-W+1+j];  dbias = sum dp; the state's rows take dx at negative i, and
+// the final state's gradient goes to the rows that it copied.  Bound by HBM:
+// x and dy read, dx written.  A thread walks L + W-1 tokens of V channels
+// once, forming p and dp and emitting dx[t-W+1] at token t; the W-1 tokens
+// behind its own L are formed twice.  dw and dbias are summed in registers,
+// over the block's walks in shared memory, and over blocks by
+// conv_reduce_kernel in a fixed order (no atomics).
+constexpr int kBX = 32, kBY = 8;  // channel groups x walks of a block
+
+template <typename T, int V, int W, bool SILU>
+__global__ void __launch_bounds__(kBX* kBY)
+conv_bwd_kernel(const T* __restrict__ x, long long ldx, const float* __restrict__ w,
+                const float* __restrict__ bias, const T* __restrict__ s0,
+                const int* __restrict__ lengths, const T* __restrict__ gy,
+                const T* __restrict__ gs, T* __restrict__ dx, T* __restrict__ ds0,
+                float* __restrict__ part, int Tn, int D, int CB, int NB, int L) {
+  const int cb = blockIdx.x % CB;
+  const int rest = blockIdx.x / CB;
+  const int nb = rest % NB, b = rest / NB;  // this block's kBY * L tokens
+  const int c = (cb * kBX + threadIdx.x) * V;
+  const bool live = c < D;
+  float dw[W][V] = {}, db[V] = {};
+  if (live) {
+    const int n = live_tokens(lengths, b, Tn);
+    const T* xb = x + (long long)b * Tn * ldx + c;
+    const T* s0b = s0 ? s0 + (long long)b * (W - 1) * D + c : nullptr;
+    const T* gb = gy + (long long)b * Tn * D + c;
+    const T* gsb = gs ? gs + (long long)b * (W - 1) * D + c : nullptr;
+    T* db_x = dx + (long long)b * Tn * D + c;
+    T* db_s = ds0 ? ds0 + (long long)b * (W - 1) * D + c : nullptr;
+    float tap[W][V], b0[V];
+    load_taps<V, W>(w, bias, c, tap, b0);
+    const int t0 = (nb * kBY + threadIdx.y) * L;
+    const int t1 = min(Tn, t0 + L);
+    if (t0 < Tn) {
+      float win[W - 1][V];     // rows t - (W-1) .. t - 1
+      float dpw[W][V] = {};    // dpw[j] = dp[t - j]
+#pragma unroll
+      for (int j = 0; j < W - 1; ++j) {
+        if (t0 - (W - 1) + j < n)  // rows at or past the length are not read
+          input_row<T, V, W>(xb, ldx, s0b, D, t0 - (W - 1) + j).get(win[j]);
+        else
+#pragma unroll
+          for (int e = 0; e < V; ++e) win[j][e] = 0.f;
+      }
+      const int emit0 = t0 == 0 ? -(W - 1) : t0;
+#pragma unroll 4
+      for (int t = t0; t < t1 + W - 1; ++t) {
+#pragma unroll
+        for (int j = W - 1; j > 0; --j)
+#pragma unroll
+          for (int e = 0; e < V; ++e) dpw[j][e] = dpw[j - 1][e];
+        if (t < n) {
+          Row<T, V> rx, rg;
+          rx.load(xb + (long long)t * ldx);
+          rg.load(gb + (long long)t * D);
+          float cur[V], g[V];
+          rx.get(cur);
+          rg.get(g);
+#pragma unroll
+          for (int e = 0; e < V; ++e) {
+            if (SILU) {
+              float p = b0[e];
+#pragma unroll
+              for (int j = 0; j < W - 1; ++j) p = fmaf(tap[j][e], win[j][e], p);
+              p = fmaf(tap[W - 1][e], cur[e], p);
+              const float s = sigmoid(p);
+              g[e] *= s * fmaf(p, 1.f - s, 1.f);
+            }
+            dpw[0][e] = g[e];
+            if (t < t1) {
+#pragma unroll
+              for (int j = 0; j < W - 1; ++j) dw[j][e] = fmaf(g[e], win[j][e], dw[j][e]);
+              dw[W - 1][e] = fmaf(g[e], cur[e], dw[W - 1][e]);
+              db[e] += g[e];
+            }
+#pragma unroll
+            for (int j = 0; j + 1 < W - 1; ++j) win[j][e] = win[j + 1][e];
+            win[W - 2][e] = cur[e];
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < V; ++e) dpw[0][e] = 0.f;
+        }
+        const int i = t - (W - 1);
+        if (i >= emit0 && i < t1) {
+          float o[V];
+#pragma unroll
+          for (int e = 0; e < V; ++e) {
+            o[e] = 0.f;
+#pragma unroll
+            for (int j = 0; j < W; ++j) o[e] = fmaf(tap[j][e], dpw[j][e], o[e]);
+          }
+          const int r = i + (W - 1) - n;  // row of the final state that holds input i
+          if (gsb && r >= 0 && r < W - 1) {
+            Row<T, V> rs;
+            float f[V];
+            rs.load(gsb + (long long)r * D);
+            rs.get(f);
+#pragma unroll
+            for (int e = 0; e < V; ++e) o[e] += f[e];
+          }
+          Row<T, V> ro;
+          ro.set(o);
+          if (i >= 0)
+            ro.store(db_x + (long long)i * D);
+          else if (db_s)
+            ro.store(db_s + (long long)(W - 1 + i) * D);
+        }
+      }
+    }
+  }
+  // block sums: [W + 1][kBX * V], one walk after the other
+  __shared__ float red[kBY][W + 1][kBX * V];
+#pragma unroll
+  for (int e = 0; e < V; ++e) {
+#pragma unroll
+    for (int j = 0; j < W; ++j) red[threadIdx.y][j][threadIdx.x * V + e] = dw[j][e];
+    red[threadIdx.y][W][threadIdx.x * V + e] = db[e];
+  }
+  __syncthreads();
+  float* pb = part + (long long)(b * NB + nb) * (W + 1) * D;
+  for (int i = threadIdx.y * kBX + threadIdx.x; i < (W + 1) * kBX * V; i += kBX * kBY) {
+    const int j = i / (kBX * V), k = i % (kBX * V);
+    float s = 0.f;
+#pragma unroll
+    for (int r = 0; r < kBY; ++r) s += red[r][j][k];
+    const int d = cb * kBX * V + k;
+    if (d < D) pb[(long long)j * D + d] = s;
+  }
+}
+
+// Sums the blocks' parts [P][W + 1][D] in order: dw[d][j], dbias[d].
+__global__ void __launch_bounds__(256)
+conv_reduce_kernel(const float* __restrict__ part, int P, int W, int D, float* __restrict__ dw,
+                   float* __restrict__ dbias) {
+  __shared__ float red[8][32];
+  const int lane = threadIdx.x & 31, row = threadIdx.x >> 5;
+  const long long i = (long long)blockIdx.x * 32 + lane, n = (long long)(W + 1) * D;
+  float s = 0.f;
+  if (i < n)
+    for (int p = row; p < P; p += 8) s += part[(long long)p * n + i];
+  red[row][lane] = s;
+  __syncthreads();
+  if (row == 0 && i < n) {
+    s = 0.f;
+#pragma unroll
+    for (int r = 0; r < 8; ++r) s += red[r][lane];
+    const int j = (int)(i / D), d = (int)(i % D);
+    if (j < W)
+      dw[(long long)d * W + j] = s;
+    else if (dbias)
+      dbias[d] = s;
+  }
+}
+
+// ---------------------------------------------------------------- one token
+//
+// y of the new token from the state's W-1 inputs, and the state moved on by
+// one in place.  A thread owns its channels of one sequence, so no other
+// thread reads what it writes.
+template <typename T, int V, int W, bool SILU>
+__global__ void __launch_bounds__(128)
+conv_step_kernel(const T* __restrict__ x, long long ldx, const float* __restrict__ w,
+                 const float* __restrict__ bias, T* __restrict__ s, T* __restrict__ y, int D,
+                 int CG, long long total) {
+  const long long id = (long long)blockIdx.x * 128 + threadIdx.x;
+  if (id >= total) return;
+  const int c = (int)(id % CG) * V;
+  const long long b = id / CG;
+  T* sb = s + b * (W - 1) * D + c;
+  Row<T, V> rows[W];
+#pragma unroll
+  for (int j = 0; j < W - 1; ++j) rows[j].load(sb + (long long)j * D);
+  rows[W - 1].load(x + b * ldx + c);
+  float tap[W][V], p[V];
+  load_taps<V, W>(w, bias, c, tap, p);
+#pragma unroll
+  for (int j = 0; j < W; ++j) {
+    float f[V];
+    rows[j].get(f);
+#pragma unroll
+    for (int e = 0; e < V; ++e) p[e] = fmaf(tap[j][e], f[e], p[e]);
+  }
+  if (SILU)
+#pragma unroll
+    for (int e = 0; e < V; ++e) p[e] = silu(p[e]);
+  Row<T, V> o;
+  o.set(p);
+  o.store(y + b * D + c);
+#pragma unroll
+  for (int j = 0; j < W - 1; ++j) rows[j + 1].store(sb + (long long)j * D);
+}
+
+// ---------------------------------------------------------------- host side
+
+// Tokens that one thread walks.  Long walks read fewer rows twice; short
+// prompts need the threads more: 16 tokens where that still gives every SM
+// 1024 threads, else 4.
+static int fwd_walk(long long B, int T, int CG) {
+  return B * ((T + 15) / 16) * CG >= 148LL * 1024 ? 16 : 4;
+}
+
+// Tokens of one backward walk (a block runs kBY of them side by side): 32,
+// and 8 where 32 would leave SMs without a block.
+static int bwd_walk(long long B, int T, int D, int V) {
+  const long long cb = (D + kBX * V - 1) / (kBX * V);
+  return B * cb * ((T + 32 * kBY - 1) / (32 * kBY)) >= 2 * 148 ? 32 : 8;
+}
+
+static long long bwd_parts(int B, int T, int D, int V) {
+  const int L = bwd_walk(B, T, D, V);
+  return (long long)B * ((T + kBY * L - 1) / (kBY * L));
+}
+
+template <typename T, int V, int W>
+static cudaError_t launch_fwd(const void* x, long long ldx, const float* w, const float* bias,
+                              const void* s0, const int* lengths, void* y, void* sT, int B,
+                              int Tn, int D, bool silu, cudaStream_t st) {
+  const int CG = D / V, L = fwd_walk(B, Tn, CG), NB = (Tn + L - 1) / L;
+  const long long total = (long long)B * NB * CG, blocks = (total + 255) / 256;
+  if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
+  auto k = silu ? conv_fwd_kernel<T, V, W, true> : conv_fwd_kernel<T, V, W, false>;
+  k<<<(unsigned)blocks, 256, 0, st>>>((const T*)x, ldx, w, bias, (const T*)s0, lengths, (T*)y,
+                                      (T*)sT, Tn, D, CG, NB, L, total);
+  return cudaGetLastError();
+}
+
+template <typename T, int V, int W>
+static cudaError_t launch_bwd(const void* x, long long ldx, const float* w, const float* bias,
+                              const void* s0, const int* lengths, const void* gy,
+                              const void* gs, void* dx, float* dw, float* dbias, void* ds0,
+                              int B, int Tn, int D, bool silu, float* part, cudaStream_t st) {
+  const int CB = (D + kBX * V - 1) / (kBX * V), L = bwd_walk(B, Tn, D, V);
+  const int NB = (Tn + kBY * L - 1) / (kBY * L);
+  const long long blocks = (long long)CB * NB * B;
+  if (blocks > 0x7fffffffLL || (long long)NB * B > 0x7fffffffLL) return cudaErrorInvalidValue;
+  auto k = silu ? conv_bwd_kernel<T, V, W, true> : conv_bwd_kernel<T, V, W, false>;
+  k<<<(unsigned)blocks, dim3(kBX, kBY), 0, st>>>((const T*)x, ldx, w, bias, (const T*)s0,
+                                                 lengths, (const T*)gy, (const T*)gs, (T*)dx,
+                                                 (T*)ds0, part, Tn, D, CB, NB, L);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  const long long n = (long long)(W + 1) * D;
+  conv_reduce_kernel<<<(unsigned)((n + 31) / 32), 256, 0, st>>>(part, B * NB, W, D, dw, dbias);
+  return cudaGetLastError();
+}
+
+template <typename T, int V, int W>
+static cudaError_t launch_step(const void* x, long long ldx, const float* w, const float* bias,
+                               void* s, void* y, int B, int D, bool silu, cudaStream_t st) {
+  const int CG = D / V;
+  const long long total = (long long)B * CG, blocks = (total + 127) / 128;
+  if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
+  auto k = silu ? conv_step_kernel<T, V, W, true> : conv_step_kernel<T, V, W, false>;
+  k<<<(unsigned)blocks, 128, 0, st>>>((const T*)x, ldx, w, bias, (T*)s, (T*)y, D, CG, total);
+  return cudaGetLastError();
+}
+
+// The checks that all three calls share.
+static kla_status check(int B, int T, int D, int W, int dtype, long long ldx) {
+  if (B < 1 || T < 0 || D < 1 || W < 1 || !dtype_ok(dtype)) return KLA_ERR_INVALID_ARG;
+  if (ldx < D || !size_ok((long long)B * (T > W ? T : W), ldx)) return KLA_ERR_INVALID_ARG;
+  if (T > kMaxTokens || W < 2 || W > 4) return KLA_ERR_UNSUPPORTED;
+  return KLA_OK;
+}
+
+#define KLA_CONV_WIDTH(W, CALL)          \
+  switch (W) {                           \
+    case 2: { constexpr int KW = 2; CALL; } break; \
+    case 3: { constexpr int KW = 3; CALL; } break; \
+    default: { constexpr int KW = 4; CALL; } break; \
+  }
+
+}  // namespace conv
+}  // namespace kla
+
+using namespace kla;
+using namespace kla::conv;
+
+extern "C" {
+
+kla_status kla_conv_fwd(const void* x, long long ldx, const float* w, const float* bias,
+                        const void* s0, const int* lengths, void* y, void* sT, int B, int T,
+                        int D, int W, int silu, int dtype, void* stream) {
+  kla_status s = check(B, T, D, W, dtype, ldx);
+  if (s != KLA_OK) return s;
+  if (T > 0 && (!x || !w || !y)) return KLA_ERR_INVALID_ARG;
+  const void* const ptrs[] = {w, bias, s0, lengths, y, sT};
+  if (misaligned(ptrs) || misplaced(x, elem(dtype))) return KLA_ERR_INVALID_ARG;
+  const int es = elem(dtype);
+  const long long rows = (long long)B * T, ns = (long long)B * (W - 1) * D;
+  const Span in[] = {span(x, rows, D, ldx, es), span(w, (long long)D * W, 4),
+                     span(bias, bias ? D : 0, 4), span(s0, s0 ? ns : 0, es),
+                     span(lengths, lengths ? B : 0, 4)};
+  const Span out[] = {span(y, rows * D, es), span(sT, sT ? ns : 0, es)};
+  if (conflicts(in, out)) return KLA_ERR_INVALID_ARG;
+  cudaStream_t st = (cudaStream_t)stream;
+  cudaError_t e = cudaSuccess;
+  if (T == 0) {
+    if (sT)
+      e = s0 ? cudaMemcpyAsync(sT, s0, ns * es, cudaMemcpyDeviceToDevice, st)
+             : cudaMemsetAsync(sT, 0, ns * es, st);
+    return e == cudaSuccess ? KLA_OK : KLA_ERR_CUDA;
+  }
+#define RUN(TY, V) \
+  KLA_CONV_WIDTH(W, (e = launch_fwd<TY, V, KW>(x, ldx, w, bias, s0, lengths, y, sT, B, T, D, \
+                                              silu != 0, st)))
+  if (dtype == KLA_BF16) {
+    if (rows_aligned(x, D, ldx, 8, es)) { RUN(__nv_bfloat16, 8) } else { RUN(__nv_bfloat16, 1) }
+  } else {
+    if (rows_aligned(x, D, ldx, 4, es)) { RUN(float, 4) } else { RUN(float, 1) }
+  }
+#undef RUN
+  return e == cudaSuccess ? KLA_OK : KLA_ERR_CUDA;
+}
+
+size_t kla_conv_bwd_workspace_size(int B, int T, int D, int W) {
+  if (check(B, T, D, W, KLA_BF16, D) != KLA_OK) return 0;
+  // the larger of the two walks' part counts, whatever the pitch turns out to be
+  const long long a = bwd_parts(B, T, D, 4), b = bwd_parts(B, T, D, 1);
+  return (size_t)(a > b ? a : b) * (W + 1) * D * sizeof(float);
+}
+
+kla_status kla_conv_bwd(const void* x, long long ldx, const float* w, const float* bias,
+                        const void* s0, const int* lengths, const void* grad_y,
+                        const void* grad_sT, void* grad_x, float* grad_w, float* grad_bias,
+                        void* grad_s0, int B, int T, int D, int W, int silu, int dtype,
+                        void* workspace, size_t ws_bytes, void* stream) {
+  kla_status s = check(B, T, D, W, dtype, ldx);
+  if (s != KLA_OK) return s;
+  if (T > 0 && (!x || !grad_y || !grad_x)) return KLA_ERR_INVALID_ARG;
+  if (!w || !grad_w) return KLA_ERR_INVALID_ARG;
+  const void* const ptrs[] = {w,      bias,   s0,        lengths, grad_y,   grad_sT,
+                              grad_x, grad_w, grad_bias, grad_s0, workspace};
+  if (misaligned(ptrs) || misplaced(x, elem(dtype))) return KLA_ERR_INVALID_ARG;
+  const size_t need = kla_conv_bwd_workspace_size(B, T, D, W);
+  if (ws_bytes < need || (need && !workspace)) return KLA_ERR_INVALID_ARG;
+  const int es = elem(dtype);
+  const long long rows = (long long)B * T, ns = (long long)B * (W - 1) * D;
+  const Span in[] = {span(x, rows, D, ldx, es), span(w, (long long)D * W, 4),
+                     span(bias, bias ? D : 0, 4), span(s0, s0 ? ns : 0, es),
+                     span(lengths, lengths ? B : 0, 4), span(grad_y, rows * D, es),
+                     span(grad_sT, grad_sT ? ns : 0, es)};
+  const Span out[] = {span(grad_x, rows * D, es), span(grad_w, (long long)D * W, 4),
+                      span(grad_bias, grad_bias ? D : 0, 4),
+                      span(grad_s0, grad_s0 ? ns : 0, es), span(workspace, (long long)need, 1)};
+  if (conflicts(in, out)) return KLA_ERR_INVALID_ARG;
+  cudaStream_t st = (cudaStream_t)stream;
+  cudaError_t e = cudaSuccess;
+  if (T == 0) {
+    e = cudaMemsetAsync(grad_w, 0, (size_t)D * W * 4, st);
+    if (e == cudaSuccess && grad_bias) e = cudaMemsetAsync(grad_bias, 0, (size_t)D * 4, st);
+    if (e == cudaSuccess && grad_s0)
+      e = grad_sT ? cudaMemcpyAsync(grad_s0, grad_sT, ns * es, cudaMemcpyDeviceToDevice, st)
+                  : cudaMemsetAsync(grad_s0, 0, ns * es, st);
+    return e == cudaSuccess ? KLA_OK : KLA_ERR_CUDA;
+  }
+#define RUN(TY, V)                                                                          \
+  KLA_CONV_WIDTH(W, (e = launch_bwd<TY, V, KW>(x, ldx, w, bias, s0, lengths, grad_y, grad_sT, \
+                                              grad_x, grad_w, grad_bias, grad_s0, B, T, D,   \
+                                              silu != 0, (float*)workspace, st)))
+  const int v = rows_aligned(x, D, ldx, 4, es) ? 4 : 1;
+  if (dtype == KLA_BF16) {
+    if (v == 4) { RUN(__nv_bfloat16, 4) } else { RUN(__nv_bfloat16, 1) }
+  } else {
+    if (v == 4) { RUN(float, 4) } else { RUN(float, 1) }
+  }
+#undef RUN
+  return e == cudaSuccess ? KLA_OK : KLA_ERR_CUDA;
+}
+
+kla_status kla_conv_step(const void* x, long long ldx, const float* w, const float* bias,
+                         void* state, void* y, int B, int D, int W, int silu, int dtype,
+                         void* stream) {
+  kla_status s = check(B, 1, D, W, dtype, ldx);
+  if (s != KLA_OK) return s;
+  if (!x || !w || !state || !y) return KLA_ERR_INVALID_ARG;
+  const void* const ptrs[] = {w, bias, state, y};
+  if (misaligned(ptrs) || misplaced(x, elem(dtype))) return KLA_ERR_INVALID_ARG;
+  const int es = elem(dtype);
+  const Span in[] = {span(x, B, D, ldx, es), span(w, (long long)D * W, 4),
+                     span(bias, bias ? D : 0, 4)};
+  const Span out[] = {span(state, (long long)B * (W - 1) * D, es),
+                      span(y, (long long)B * D, es)};
+  if (conflicts(in, out)) return KLA_ERR_INVALID_ARG;
+  cudaStream_t st = (cudaStream_t)stream;
+  cudaError_t e = cudaSuccess;
+#define RUN(TY, V)                                                                           \
+  KLA_CONV_WIDTH(W, (e = launch_step<TY, V, KW>(x, ldx, w, bias, state, y, B, D, silu != 0, \
+                                               st)))
+  if (dtype == KLA_BF16) {
+    if (rows_aligned(x, D, ldx, 4, es)) { RUN(__nv_bfloat16, 4) } else { RUN(__nv_bfloat16, 1) }
+  } else {
+    if (rows_aligned(x, D, ldx, 4, es)) { RUN(float, 4) } else { RUN(float, 1) }
+  }
+#undef RUN
+  return e == cudaSuccess ? KLA_OK : KLA_ERR_CUDA;
+}
+
+}  // extern "C"

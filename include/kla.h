@@ -415,6 +415,148 @@ KLA_API kla_status kla_gdn_recurrent_bwd(const void *q, const void *k, const voi
                                          void *stream);
 
 /*
+ * Layer operators around the recurrences: what makes their inputs (short
+ * causal convolution, norm and rotation of queries and keys) and a diagonal
+ * recurrence beside them (selective state space scan).  The conventions at
+ * the top hold, with these differences:
+ *   * Inputs marked [ld] may be rows of a wider matrix (a projection's
+ *     output): row r (token b * T + t) starts ld elements after row r - 1, and
+ *     its elements are contiguous.  ld is at least the row's length.  They
+ *     need only their element's alignment (q and k of the norm: 16 bytes).
+ *   * Gradients of activations have the activations' type, gradients of
+ *     parameters and of fp32 states are fp32.
+ *   * lengths ([B] int32 on the device, nullable): sequence b has
+ *     min(max(lengths[b], 0), T) tokens.  The tokens behind are not read,
+ *     whatever they hold; their outputs and gradients are written as zeros,
+ *     and the final state is the one after the last token that exists.
+ *   * T <= 2^30.  Sums over tokens and channels are taken in a fixed order (no
+ *     atomics): the same call gives the same bits.
+ *
+ * Short causal depthwise convolution (arXiv 2312.00752, section 3.4, puts it
+ * in front of the scan; delta-rule layers put it in front of q, k and v):
+ *
+ *   p[t][d] = bias[d] + sum_{j<W} w[d][j] x[t-W+1+j][d]
+ *   y = silu ? p * sigmoid(p) : p
+ *
+ *   x   [B][T][D]   dtype [ld]  inputs
+ *   w   [D][W] fp32, bias [D] fp32 (nullable)
+ *   s0  [B][W-1][D] dtype  the last W-1 inputs before x, oldest first; NULL = 0
+ *   y   [B][T][D]   dtype  written
+ *   sT  [B][W-1][D] dtype  the last W-1 inputs (of s0 and x) written; NULL =
+ *                          not returned.  It may not overlap s0.
+ * W in {2, 3, 4} (else KLA_ERR_UNSUPPORTED); T = 0 copies s0 to sT.
+ *
+ * kla_conv_bwd: grad_sT (nullable = 0) and grad_s0 (nullable = not computed)
+ * as sT and s0; grad_x dtype, grad_w [D][W] and grad_bias [D] (nullable) fp32;
+ * workspace of kla_conv_bwd_workspace_size(...) bytes.
+ * kla_conv_step: one token for each of B sequences: x, y [B][D], and state
+ * [B][W-1][D] moved on in place.
+ */
+KLA_API kla_status kla_conv_fwd(const void *x, long long ldx, const float *w, const float *bias,
+                                const void *s0, const int *lengths, void *y, void *sT,
+                                int B, int T, int D, int W, int silu, int dtype, void *stream);
+KLA_API size_t kla_conv_bwd_workspace_size(int B, int T, int D, int W);
+KLA_API kla_status kla_conv_bwd(const void *x, long long ldx, const float *w, const float *bias,
+                                const void *s0, const int *lengths, const void *grad_y,
+                                const void *grad_sT, void *grad_x, float *grad_w,
+                                float *grad_bias, void *grad_s0, int B, int T, int D, int W,
+                                int silu, int dtype, void *workspace, size_t ws_bytes,
+                                void *stream);
+KLA_API kla_status kla_conv_step(const void *x, long long ldx, const float *w, const float *bias,
+                                 void *state, void *y, int B, int D, int W, int silu, int dtype,
+                                 void *stream);
+
+/*
+ * Selective state space scan (arXiv 2312.00752, sections 2 and 3.2, with A
+ * diagonal): per channel d of group g = d / (D / G) and state n < N
+ *
+ *   s[t][d] = dt[t][d] + dt_bias[d], through log(1 + e^s) when softplus
+ *   h[d][n] <- e^{s A[d][n]} h[d][n] + s u[t][d] Bm[t][g][n]
+ *   y[t][d]  = (sum_n Cm[t][g][n] h[d][n] + Dw[d] u[t][d]) * z sigmoid(z)
+ *
+ *   u, dt  [B][T][D] dtype [ldu, lddt];  Bm, Cm [B][T][G][N] dtype [ldb, ldc]
+ *   z      [B][T][D] dtype [ldz]  gate; NULL = no gate
+ *   A      [D][N] fp32;  Dw, dt_bias [D] fp32 (nullable = 0)
+ *   h0     [B][D][N] fp32  initial state; NULL = zeros
+ *   y      [B][T][D] dtype written;  hT [B][D][N] fp32 written, NULL = not
+ *          returned; hT may be exactly h0.
+ * N in {8, 16, 32, 64} (else KLA_ERR_UNSUPPORTED); G divides D; T = 0 copies
+ * h0 to hT.  States and sums are fp32.  Workspace: kla_ssm_fwd_workspace_size
+ * (segment states where the sequence is cut to fill the GPU; 0 otherwise).
+ *
+ * kla_ssm_bwd: every gradient for grad_y and grad_hT (nullable = 0); grad_D,
+ * grad_dt_bias, grad_h0 nullable (not computed), grad_z needed with z.
+ * Workspace kla_ssm_bwd_workspace_size(...): a state every 16 tokens
+ * (B * T * D * N / 4 bytes) and parts of the sums over channels and tokens.
+ * kla_ssm_step: one token for each of B sequences (u, dt, z, y [B][D], Bm, Cm
+ * [B][G][N]); state [B][D][N] fp32 moved on in place.
+ */
+KLA_API size_t kla_ssm_fwd_workspace_size(int B, int T, int D, int G, int N);
+KLA_API kla_status kla_ssm_fwd(const void *u, const void *dt, const float *A, const void *Bm,
+                               const void *Cm, const float *Dw, const void *z,
+                               const float *dt_bias, const float *h0, const int *lengths,
+                               void *y, float *hT, int B, int T, int D, int G, int N,
+                               long long ldu, long long lddt, long long ldb, long long ldc,
+                               long long ldz, int softplus, int dtype, void *workspace,
+                               size_t ws_bytes, void *stream);
+KLA_API size_t kla_ssm_bwd_workspace_size(int B, int T, int D, int G, int N);
+KLA_API kla_status kla_ssm_bwd(const void *u, const void *dt, const float *A, const void *Bm,
+                               const void *Cm, const float *Dw, const void *z,
+                               const float *dt_bias, const float *h0, const int *lengths,
+                               const void *grad_y, const float *grad_hT, void *grad_u,
+                               void *grad_dt, float *grad_A, void *grad_B, void *grad_C,
+                               float *grad_D, void *grad_z, float *grad_dt_bias,
+                               float *grad_h0, int B, int T, int D, int G, int N,
+                               long long ldu, long long lddt, long long ldb, long long ldc,
+                               long long ldz, int softplus, int dtype, void *workspace,
+                               size_t ws_bytes, void *stream);
+KLA_API kla_status kla_ssm_step(const void *u, const void *dt, const float *A, const void *Bm,
+                                const void *Cm, const float *Dw, const void *z,
+                                const float *dt_bias, float *state, void *y, int B, int D,
+                                int G, int N, long long ldu, long long lddt, long long ldb,
+                                long long ldc, long long ldz, int softplus, int dtype,
+                                void *stream);
+
+/*
+ * Norm of every head of q and k and its rotation by position, in one pass
+ * (gated delta-rule layers normalise q and k: "Deep Dive into KDA", section
+ * 2.2; the rotation is that of arXiv 2104.09864, section 3.2).
+ *
+ *   norm 0: x^ = x;  1 (L2): x^ = x / sqrt(sum x^2 + eps);
+ *   norm 2 (RMS): x^ = x / sqrt(sum x^2 / d + eps)
+ *   out = w x^, its first rot channels turned: pair i by the angle
+ *   position * inv_freq[i], cosine and sine times scale; pairs are
+ *   (i, i + rot/2), or (2i, 2i+1) when interleaved.
+ *
+ *   q [B][T][Hq][d] dtype [ldq], k [B][T][Hk][d] dtype [ldk] (Hq or Hk may be 0)
+ *   wq, wk [d] fp32, nullable = 1;  inv_freq [rot/2] fp32 (rot = 0: none)
+ *   positions: int32 [B][T] with rows pos_stride apart (0: one row for all
+ *   sequences); NULL = pos0 + t.  Angles are formed in fp64.
+ *   oq, ok: contiguous, dtype, written.
+ * d a multiple of 8, at most 256; ldq and ldk multiples of 16 bytes (else
+ * KLA_ERR_UNSUPPORTED); rot even, at most d.  Inverse frequencies stretched
+ * for longer contexts, and the scale that goes with them, are the caller's.
+ * kla_qk_norm_bwd: grad_q, grad_k from grad_oq, grad_ok; grad_wq, grad_wk
+ * [d] fp32 (nullable = not computed; with either, a workspace of
+ * kla_qk_norm_bwd_workspace_size(...) bytes).
+ */
+KLA_API kla_status kla_qk_norm_fwd(const void *q, const void *k, long long ldq, long long ldk,
+                                   const float *wq, const float *wk, const int *positions,
+                                   long long pos_stride, int pos0, const float *inv_freq,
+                                   int rot, int interleaved, float scale, int norm, float eps,
+                                   void *oq, void *ok, int B, int T, int Hq, int Hk, int d,
+                                   int dtype, void *stream);
+KLA_API size_t kla_qk_norm_bwd_workspace_size(int B, int T, int Hq, int Hk, int d, int rot);
+KLA_API kla_status kla_qk_norm_bwd(const void *q, const void *k, long long ldq, long long ldk,
+                                   const float *wq, const float *wk, const int *positions,
+                                   long long pos_stride, int pos0, const float *inv_freq,
+                                   int rot, int interleaved, float scale, int norm, float eps,
+                                   const void *grad_oq, const void *grad_ok, void *grad_q,
+                                   void *grad_k, float *grad_wq, float *grad_wk, int B, int T,
+                                   int Hq, int Hk, int d, int dtype, void *workspace,
+                                   size_t ws_bytes, void *stream);
+
+/*
  * Prefill from HOST buffers, end to end: the same computation as
  * kla_chunk_fwd with q, k, v, g, eta, h0 (nullable), o and hT (nullable) in
  * host memory (same layouts; page-locked memory is needed for the copies to
