@@ -31,7 +31,7 @@ namespace ssm {
 using namespace layer;
 
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr int kTile = 32;     // tokens of a tile of the forward scan
+constexpr int kTile = 32;     // segments are multiples of this many tokens
 constexpr int kCW = 4;        // warps that run the recurrence
 constexpr int kCkpt = 16;     // tokens between the backward's saved states
 
@@ -42,6 +42,13 @@ struct Shape {
   static constexpr int LPC = N / 4;                  // lanes of a channel
   static constexpr int CPT = N == 8 ? 1 : 2;         // channels of a thread
   static constexpr int CH = kCW * (32 / LPC) * CPT;  // channels of a block
+};
+
+// Tokens of a tile of the forward scan: what a helper thread's registers hold
+// of three tiles, and at least four channels of one token each.
+template <typename T, int N>
+struct Tile {
+  static constexpr int TK = sizeof(T) == 2 || N == 64 ? 32 : 16;
 };
 
 struct Args {
@@ -84,19 +91,29 @@ __device__ __forceinline__ float step_of(float raw, bool sp) { return sp ? softp
 // Forward scan of one (channel tile, sequence, segment).
 // REV (LOCAL only): the adjoint state e[t] = a[t] (e[t+1] + C[t] g[t]), g =
 // gy silu(z), from the segment's last token to its first.
+//
+// A helper thread keeps its four channels through the sequence, loads its
+// rows of the tile after the next into registers before it works on the next
+// (a tile's time covers the latency), and holds u and z until the tile's y is
+// there.
 template <typename T, int N, int MODE, bool REV>
 __global__ void __launch_bounds__(2 * kCW * 32)
 scan_kernel(Args p) {
   constexpr int LPC = Shape<N>::LPC, CPT = Shape<N>::CPT, CH = Shape<N>::CH;
+  constexpr int TK = Tile<T, N>::TK;
   constexpr int CPW = CH / kCW;  // channels of a warp
+  constexpr int NH = kCW * 32;   // helper threads
+  constexpr int IX = TK * CH / 4 / NH;                      // channel groups of a helper
+  constexpr int IB = (TK * N / 4 + NH - 1) / NH;            // groups of B and of C
+  static_assert(IX * NH * 4 == TK * CH && NH % (CH / 4) == 0, "helpers share a tile evenly");
   static_assert(!REV || MODE == LOCAL, "only end states run backward");
+  constexpr bool USE_B = !REV, USE_C = MODE == FULL || REV;
   extern __shared__ __align__(16) unsigned char smem_raw[];
-  // [2][kTile][CH] (dt', dt' u) or (dt', g); [2][kTile][N] B and C;
-  // [2][kTile][CH] y
+  // [2][TK][CH] (dt', dt' u) or (dt', g); [2][TK][N] B and C; [2][TK][CH] y
   float2* s_x = reinterpret_cast<float2*>(smem_raw);
-  float* s_b = reinterpret_cast<float*>(s_x + 2 * kTile * CH);
-  float* s_c = s_b + 2 * kTile * N;
-  float* s_y = s_c + 2 * kTile * N;
+  float* s_b = reinterpret_cast<float*>(s_x + 2 * TK * CH);
+  float* s_c = s_b + 2 * TK * N;
+  float* s_y = s_c + 2 * TK * N;
 
   const int Dg = p.D / p.G, TPG = (Dg + CH - 1) / CH;
   const int tiles = TPG * p.G;
@@ -107,204 +124,245 @@ scan_kernel(Args p) {
   const int c0 = g * Dg + (ct % TPG) * CH;       // first channel
   const int nc = min(CH, (g + 1) * Dg - c0);     // channels that exist
   const int t_lo = sg * p.seg, t_hi = min(p.T, t_lo + p.seg);
-  const int n_live = live_tokens(p.lengths, b, p.T);
-  const int ntile = (t_hi - t_lo + kTile - 1) / kTile;
+  const int t_live = min(t_hi, live_tokens(p.lengths, b, p.T));
+  const int ntile = (t_hi - t_lo + TK - 1) / TK;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const bool compute = warp < kCW;
+  const int first = REV ? ntile - 1 : 0, dir = REV ? -1 : 1;
   const long long row0 = (long long)b * p.T;
 
-  const T* u = (const T*)p.u + c0;
-  const T* dt = (const T*)p.dt + c0;
-  const T* z = p.z ? (const T*)p.z + c0 : nullptr;
-  const T* gy = (const T*)p.gy + c0;
-  const T* Bm = (const T*)p.Bm + (long long)g * N;
-  const T* Cm = (const T*)p.Cm + (long long)g * N;
-  const bool vec = (Dg & 3) == 0, vy = vec;
-  const bool vu = vec && p.vu, vdt = vec && p.vdt, vz = vec && p.vz, vb = p.vb, vc = p.vc;
+  if (warp >= kCW) {
+    // ------------------------------------------------ helpers
+    const int hid = tid - NH;
+    const int c = (hid % (CH / 4)) * 4, tt0 = hid / (CH / 4);
+    constexpr int TS = NH / (CH / 4);  // tokens between a helper's groups
+    const int m = nc - c;              // channels that exist of this thread's four
+    const bool vec = (Dg & 3) == 0;
+    const bool vu = vec && p.vu, vdt = vec && p.vdt, vz = vec && p.vz;
+    const T* src = REV ? (const T*)p.gy : (const T*)p.u;  // u, or gy
+    const long long lds = REV ? p.D : p.ldu;
+    const bool vs = REV ? vec : vu;
+    src += row0 * lds + c0 + c;
+    const T* dt = (const T*)p.dt + row0 * p.lddt + c0 + c;
+    const bool has_z = p.z && (MODE == FULL || REV);
+    const T* z = has_z ? (const T*)p.z + row0 * p.ldz + c0 + c : nullptr;
+    const T* Bm = (const T*)p.Bm + row0 * p.ldb + (long long)g * N;
+    const T* Cm = (const T*)p.Cm + row0 * p.ldc + (long long)g * N;
+    T* y = MODE == FULL ? (T*)p.y + row0 * p.D + c0 + c : nullptr;
+    const bool sp = p.softplus != 0;
+    float4 bias = make_float4(0.f, 0.f, 0.f, 0.f), skip = bias;
+    if (p.bias) bias = ld4(p.bias + c0 + c, m, vec);
+    if (MODE == FULL && p.Dw) skip = ld4(p.Dw + c0 + c, m, vec);
 
-  // helper warps: tile k's inputs into buffer k & 1
-  const int hid = tid - kCW * 32;
-  auto stage = [&](int k) {
-    const int t0 = t_lo + k * kTile;
-    float2* sx = s_x + (k & 1) * kTile * CH;
-    float* sb = s_b + (k & 1) * kTile * N;
-    float* sc = s_c + (k & 1) * kTile * N;
-#pragma unroll 2
-    for (int i = hid; i < kTile * CH / 4; i += kCW * 32) {
-      const int tt = i / (CH / 4), c = (i % (CH / 4)) * 4, t = t0 + tt;
-      float4 d = make_float4(0.f, 0.f, 0.f, 0.f), x = d;
-      if (t < t_hi && t < n_live && c < nc) {
-        const long long r = row0 + t;
-        const int m = nc - c;
-        d = ld4(dt + r * p.lddt + c, m, vdt);
-        if (p.bias) {
-          const float4 q = ld4(p.bias + c0 + c, m, vec);
-          d.x += q.x; d.y += q.y; d.z += q.z; d.w += q.w;
+    Raw4<T> xn[IX], dn[IX], zn[IX], bn[IB], cn[IB];  // the tile to be staged next
+    Raw4<T> xc[IX], zc[IX], xp[IX], zp[IX];          // u, z of the tiles in the scan and done
+    auto load = [&](int k) {
+      const int t0 = t_lo + k * TK;
+#pragma unroll
+      for (int i = 0; i < IX; ++i) {
+        const int t = t0 + tt0 + i * TS;
+        const int n = t < t_live ? m : 0;
+        xn[i] = ld_raw4(src + (long long)t * lds, n, vs);
+        dn[i] = ld_raw4(dt + (long long)t * p.lddt, n, vdt);
+        if (has_z) zn[i] = ld_raw4(z + (long long)t * p.ldz, n, vz);
+      }
+#pragma unroll
+      for (int i = 0; i < IB; ++i) {
+        const int j = hid + i * NH, t = t0 + j / (N / 4), n = (j % (N / 4)) * 4;
+        const int e = j < TK * N / 4 && t < t_live ? 4 : 0;
+        if (USE_B) bn[i] = ld_raw4(Bm + (long long)t * p.ldb + n, e, p.vb);
+        if (USE_C) cn[i] = ld_raw4(Cm + (long long)t * p.ldc + n, e, p.vc);
+      }
+    };
+    auto stage = [&](int k) {
+      const int t0 = t_lo + k * TK;
+      float2* sx = s_x + (k & 1) * TK * CH;
+#pragma unroll
+      for (int i = 0; i < IX; ++i) {
+        const int tt = tt0 + i * TS;
+        float4 d = dn[i].get(), x = xn[i].get();
+        d.x += bias.x; d.y += bias.y; d.z += bias.z; d.w += bias.w;
+        if (sp) {
+          d.x = softplus(d.x); d.y = softplus(d.y); d.z = softplus(d.z); d.w = softplus(d.w);
         }
-        d.x = step_of(d.x, p.softplus); d.y = step_of(d.y, p.softplus);
-        d.z = step_of(d.z, p.softplus); d.w = step_of(d.w, p.softplus);
+        // tokens that do not exist, and channels past the last, step by 0:
+        // their state stays as it is
+        const int n = t0 + tt < t_live ? m : 0;
+        if (n < 4) {
+          if (n < 1) d.x = 0.f;
+          if (n < 2) d.y = 0.f;
+          if (n < 3) d.z = 0.f;
+          d.w = 0.f;
+        }
         if (REV) {
-          x = ld4(gy + r * p.D + c, m, vy);
-          if (z) {
-            const float4 q = ld4(z + r * p.ldz + c, m, vz);
+          if (has_z) {
+            const float4 q = zn[i].get();
             x.x *= silu(q.x); x.y *= silu(q.y); x.z *= silu(q.z); x.w *= silu(q.w);
           }
         } else {
-          x = ld4(u + r * p.ldu + c, m, vu);
           x.x *= d.x; x.y *= d.y; x.z *= d.z; x.w *= d.w;
         }
-        // channels past the tile's last keep a zero step: their state stays 0
-        if (m < 4) {
-          if (m < 2) d.y = x.y = 0.f;
-          if (m < 3) d.z = x.z = 0.f;
-          d.w = x.w = 0.f;
+        float4* o = reinterpret_cast<float4*>(sx + tt * CH + c);
+        o[0] = make_float4(d.x, x.x, d.y, x.y);
+        o[1] = make_float4(d.z, x.z, d.w, x.w);
+      }
+#pragma unroll
+      for (int i = 0; i < IB; ++i) {
+        const int j = hid + i * NH;
+        if (j < TK * N / 4) {
+          if (USE_B) reinterpret_cast<float4*>(s_b + (k & 1) * TK * N)[j] = bn[i].get();
+          if (USE_C) reinterpret_cast<float4*>(s_c + (k & 1) * TK * N)[j] = cn[i].get();
         }
       }
-      float4* o = reinterpret_cast<float4*>(sx + tt * CH + c);
-      o[0] = make_float4(d.x, x.x, d.y, x.y);
-      o[1] = make_float4(d.z, x.z, d.w, x.w);
-    }
-    for (int i = hid; i < kTile * N / 4; i += kCW * 32) {
-      const int tt = i / (N / 4), n = (i % (N / 4)) * 4, t = t0 + tt;
-      float4 vb4 = make_float4(0.f, 0.f, 0.f, 0.f), vc4 = vb4;
-      if (t < t_hi && t < n_live) {
-        if (!REV) vb4 = ld4(Bm + (row0 + t) * p.ldb + n, 4, vb);
-        if (MODE == FULL || REV) vc4 = ld4(Cm + (row0 + t) * p.ldc + n, 4, vc);
-      }
-      if (!REV) *reinterpret_cast<float4*>(sb + tt * N + n) = vb4;
-      if (MODE == FULL || REV) *reinterpret_cast<float4*>(sc + tt * N + n) = vc4;
-    }
-  };
-  // helper warps: tile k's y from buffer k & 1
-  auto finish = [&](int k) {
-    const int t0 = t_lo + k * kTile;
-    const float* sy = s_y + (k & 1) * kTile * CH;
-    T* y = (T*)p.y + c0;
-#pragma unroll 2
-    for (int i = hid; i < kTile * CH / 4; i += kCW * 32) {
-      const int tt = i / (CH / 4), c = (i % (CH / 4)) * 4, t = t0 + tt;
-      if (t >= t_hi || c >= nc) continue;
-      const long long r = row0 + t;
-      const int m = nc - c;
-      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (t < n_live) {
-        v = *reinterpret_cast<const float4*>(sy + tt * CH + c);
-        if (p.Dw) {
-          const float4 w = ld4(p.Dw + c0 + c, m, vec), q = ld4(u + r * p.ldu + c, m, vu);
-          v.x = fmaf(w.x, q.x, v.x); v.y = fmaf(w.y, q.y, v.y);
-          v.z = fmaf(w.z, q.z, v.z); v.w = fmaf(w.w, q.w, v.w);
+    };
+    auto finish = [&](int k, const Raw4<T>(&xs)[IX], const Raw4<T>(&zs)[IX]) {
+      const int t0 = t_lo + k * TK;
+      const float* sy = s_y + (k & 1) * TK * CH;
+#pragma unroll
+      for (int i = 0; i < IX; ++i) {
+        const int tt = tt0 + i * TS, t = t0 + tt;
+        if (t >= t_hi || m <= 0) continue;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (t < t_live) {
+          const float4 q = xs[i].get();
+          v = *reinterpret_cast<const float4*>(sy + tt * CH + c);
+          v.x = fmaf(skip.x, q.x, v.x); v.y = fmaf(skip.y, q.y, v.y);
+          v.z = fmaf(skip.z, q.z, v.z); v.w = fmaf(skip.w, q.w, v.w);
+          if (has_z) {
+            const float4 w = zs[i].get();
+            v.x *= silu(w.x); v.y *= silu(w.y); v.z *= silu(w.z); v.w *= silu(w.w);
+          }
         }
-        if (z) {
-          const float4 q = ld4(z + r * p.ldz + c, m, vz);
-          v.x *= silu(q.x); v.y *= silu(q.y); v.z *= silu(q.z); v.w *= silu(q.w);
-        }
+        st4(y + (long long)t * p.D, v, m, vec);
       }
-      st4(y + r * p.D + c, v, m, vy);
+    };
+    if (ntile > 0) {
+      load(first);
+      stage(first);
     }
-  };
+#pragma unroll
+    for (int i = 0; i < IX; ++i) { xc[i] = xn[i]; zc[i] = zn[i]; }
+    if (ntile > 1) load(first + dir);
+    __syncthreads();
+    for (int i = 0; i < ntile; ++i) {
+      const int k = first + dir * i;
+      if (i + 1 < ntile) stage(k + dir);
+      if (MODE == FULL && i > 0) finish(k - dir, xp, zp);
+#pragma unroll
+      for (int j = 0; j < IX; ++j) {
+        xp[j] = xc[j]; zp[j] = zc[j];
+        xc[j] = xn[j]; zc[j] = zn[j];
+      }
+      if (i + 2 < ntile) load(k + 2 * dir);
+      __syncthreads();
+    }
+    if (MODE == FULL && ntile > 0) finish(ntile - 1, xp, zp);
+    return;
+  }
 
-  // recurrence warps: 4 states of CPT channels
-  const int nl = lane % LPC, cl = warp * CPW + (lane / LPC) * CPT;
-  const int cc = compute ? cl : 0;
-  float a2[CPT][4], h[CPT][4], sum[CPT];
-  if (compute) {
+  // -------------------------------------------------- recurrence: 4 states of
+  // CPT channels, as pairs
+  const int nl = lane % LPC, cc = warp * CPW + (lane / LPC) * CPT;
+  f32x2 a2[CPT][2], h[CPT][2];
+  float sum[CPT];
 #pragma unroll
-    for (int k = 0; k < CPT; ++k) {
-      sum[k] = 0.f;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) a2[k][i] = h[k][i] = 0.f;
-      if (cc + k < nc) {
-        const long long at = (long long)(c0 + cc + k) * N + nl * 4;
-        const float4 v = *reinterpret_cast<const float4*>(p.A + at);
-        a2[k][0] = v.x * kLog2e; a2[k][1] = v.y * kLog2e;
-        a2[k][2] = v.z * kLog2e; a2[k][3] = v.w * kLog2e;
-        const float* from = nullptr;
-        if (MODE != LOCAL) {
-          if (p.S > 1)
-            from = p.ends + ((long long)b * p.S + sg) * p.D * N + at;
-          else if (p.h0)
-            from = p.h0 + (long long)b * p.D * N + at;
-        }
-        if (from) {
-          const float4 q = *reinterpret_cast<const float4*>(from);
-          h[k][0] = q.x; h[k][1] = q.y; h[k][2] = q.z; h[k][3] = q.w;
-        }
+  for (int k = 0; k < CPT; ++k) {
+    sum[k] = 0.f;
+    a2[k][0] = a2[k][1] = h[k][0] = h[k][1] = pack2(0.f, 0.f);
+    if (cc + k < nc) {
+      const long long at = (long long)(c0 + cc + k) * N + nl * 4;
+      const float4 v = *reinterpret_cast<const float4*>(p.A + at);
+      a2[k][0] = pack2(v.x * kLog2e, v.y * kLog2e);
+      a2[k][1] = pack2(v.z * kLog2e, v.w * kLog2e);
+      const float* from = nullptr;
+      if (MODE != LOCAL) {
+        if (p.S > 1)
+          from = p.ends + ((long long)b * p.S + sg) * p.D * N + at;
+        else if (p.h0)
+          from = p.h0 + (long long)b * p.D * N + at;
+      }
+      if (from) {
+        const float4 q = *reinterpret_cast<const float4*>(from);
+        h[k][0] = pack2(q.x, q.y);
+        h[k][1] = pack2(q.z, q.w);
       }
     }
   }
   auto save = [&](float* to) {  // to: [D][N]
 #pragma unroll
     for (int k = 0; k < CPT; ++k)
-      if (cc + k < nc)
+      if (cc + k < nc) {
+        const float2 u = unpack2(h[k][0]), v = unpack2(h[k][1]);
         *reinterpret_cast<float4*>(to + (long long)(c0 + cc + k) * N + nl * 4) =
-            make_float4(h[k][0], h[k][1], h[k][2], h[k][3]);
+            make_float4(u.x, u.y, v.x, v.y);
+      }
   };
   auto scan = [&](int k) {
-    const float2* sx = s_x + (k & 1) * kTile * CH + cc;
-    const float* sb = s_b + (k & 1) * kTile * N + nl * 4;
-    const float* sc = s_c + (k & 1) * kTile * N + nl * 4;
-    float* sy = s_y + (k & 1) * kTile * CH + cc;
-    constexpr int UN = MODE == FULL ? LPC : 4;  // tokens of one y exchange
+    const float2* sx = s_x + (k & 1) * TK * CH + cc;
+    const float* sb = s_b + (k & 1) * TK * N + nl * 4;
+    const float* sc = s_c + (k & 1) * TK * N + nl * 4;
+    float* sy = s_y + (k & 1) * TK * CH + cc;
+    constexpr int UN = MODE == FULL ? (LPC > 4 ? LPC : 4) : 4;
 #pragma unroll 1
-    for (int tt = 0; tt < kTile; tt += UN) {
+    for (int tt = 0; tt < TK; tt += UN) {
       if (MODE == CKPT && tt % kCkpt == 0) {
-        const int t = t_lo + k * kTile + tt;
+        const int t = t_lo + k * TK + tt;
         if (t < t_hi)
           save(p.ckpt + ((long long)b * ((p.T + kCkpt - 1) / kCkpt) + t / kCkpt) * p.D * N);
       }
       float yv[UN][CPT];
 #pragma unroll
       for (int i = 0; i < UN; ++i) {
-        const int t = REV ? kTile - 1 - tt - i : tt + i;
-        float4 bv, cv;
-        if (!REV) bv = *reinterpret_cast<const float4*>(sb + t * N);
-        if (MODE == FULL || REV) cv = *reinterpret_cast<const float4*>(sc + t * N);
+        const int t = REV ? TK - 1 - tt - i : tt + i;
+        f32x2 bv[2], cv[2];
+        if (USE_B) {
+          const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(sb + t * N);
+          bv[0] = v.x; bv[1] = v.y;
+        }
+        if (USE_C) {
+          const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(sc + t * N);
+          cv[0] = v.x; cv[1] = v.y;
+        }
+        float2 x[CPT];
+        if constexpr (CPT == 2) {
+          const float4 v = *reinterpret_cast<const float4*>(sx + t * CH);
+          x[0] = make_float2(v.x, v.y);
+          x[1] = make_float2(v.z, v.w);
+        } else {
+          x[0] = sx[t * CH];
+        }
 #pragma unroll
         for (int c = 0; c < CPT; ++c) {
-          const float2 x = sx[t * CH + c];
-          const float a0 = ex2(x.x * a2[c][0]), a1 = ex2(x.x * a2[c][1]),
-                      a2_ = ex2(x.x * a2[c][2]), a3 = ex2(x.x * a2[c][3]);
+          const f32x2 d2 = pack2(x[c].x, x[c].x), w2 = pack2(x[c].y, x[c].y);
+          const f32x2 e0 = ex2_2(mul2(d2, a2[c][0])), e1 = ex2_2(mul2(d2, a2[c][1]));
           if (REV) {
-            h[c][0] = a0 * fmaf(x.y, cv.x, h[c][0]);
-            h[c][1] = a1 * fmaf(x.y, cv.y, h[c][1]);
-            h[c][2] = a2_ * fmaf(x.y, cv.z, h[c][2]);
-            h[c][3] = a3 * fmaf(x.y, cv.w, h[c][3]);
+            h[c][0] = mul2(e0, fma2(w2, cv[0], h[c][0]));
+            h[c][1] = mul2(e1, fma2(w2, cv[1], h[c][1]));
           } else {
-            h[c][0] = fmaf(a0, h[c][0], x.y * bv.x);
-            h[c][1] = fmaf(a1, h[c][1], x.y * bv.y);
-            h[c][2] = fmaf(a2_, h[c][2], x.y * bv.z);
-            h[c][3] = fmaf(a3, h[c][3], x.y * bv.w);
+            h[c][0] = fma2(e0, h[c][0], mul2(w2, bv[0]));
+            h[c][1] = fma2(e1, h[c][1], mul2(w2, bv[1]));
           }
-          if (MODE == LOCAL) sum[c] += x.x;
-          if (MODE == FULL)
-            yv[i][c] = fmaf(cv.w, h[c][3], fmaf(cv.z, h[c][2], fmaf(cv.y, h[c][1],
-                                                                    cv.x * h[c][0])));
+          if (MODE == LOCAL) sum[c] += x[c].x;
+          if (MODE == FULL) {
+            const float2 s = unpack2(fma2(cv[1], h[c][1], mul2(cv[0], h[c][0])));
+            yv[i][c] = s.x + s.y;
+          }
         }
       }
       if constexpr (MODE == FULL) {
-        scatter_sum<LPC, CPT>(yv, nl);
 #pragma unroll
-        for (int c = 0; c < CPT; ++c) sy[(tt + nl) * CH + c] = yv[0][c];
+        for (int j = 0; j < UN; j += LPC) {
+          float (&part)[LPC][CPT] = *reinterpret_cast<float (*)[LPC][CPT]>(&yv[j]);
+          scatter_sum<LPC, CPT>(part, nl);
+#pragma unroll
+          for (int c = 0; c < CPT; ++c) sy[(tt + j + nl) * CH + c] = part[0][c];
+        }
       }
     }
   };
-
-  const int first = REV ? ntile - 1 : 0, dir = REV ? -1 : 1;
-  if (!compute) stage(first);
   __syncthreads();
   for (int i = 0; i < ntile; ++i) {
-    const int k = first + dir * i;
-    if (compute) {
-      scan(k);
-    } else {
-      if (i + 1 < ntile) stage(k + dir);
-      if (MODE == FULL && i > 0) finish(k - dir);
-    }
+    scan(first + dir * i);
     __syncthreads();
-  }
-  if (!compute) {
-    if (MODE == FULL && ntile > 0) finish(ntile - 1);
-    return;
   }
   if (MODE == LOCAL) {
     save(p.ends + ((long long)b * p.S + sg) * p.D * N);
@@ -782,7 +840,7 @@ static size_t chain_bytes(int B, int D, int N, int S) {
 template <typename T, int N, int MODE, bool REV>
 static cudaError_t run_scan(const Args& a, cudaStream_t st) {
   constexpr int CH = Shape<N>::CH;
-  const size_t smem = 2 * kTile * (CH * (8 + (MODE == FULL ? 4 : 0)) + 2 * N * 4);
+  const size_t smem = 2 * Tile<T, N>::TK * (CH * (8 + (MODE == FULL ? 4 : 0)) + 2 * N * 4);
   const long long blocks = tiles_of(a.D, a.G, CH) * a.B * a.S;
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
   auto k = scan_kernel<T, N, MODE, REV>;
