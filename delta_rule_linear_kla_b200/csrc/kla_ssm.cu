@@ -97,7 +97,7 @@ __device__ __forceinline__ float step_of(float raw, bool sp) { return sp ? softp
 // (a tile's time covers the latency), and holds u and z until the tile's y is
 // there.
 template <typename T, int N, int MODE, bool REV>
-__global__ void __launch_bounds__(2 * kCW * 32)
+__global__ void __launch_bounds__(2 * kCW * 32, 2)
 scan_kernel(Args p) {
   constexpr int LPC = Shape<N>::LPC, CPT = Shape<N>::CPT, CH = Shape<N>::CH;
   constexpr int TK = Tile<T, N>::TK;
