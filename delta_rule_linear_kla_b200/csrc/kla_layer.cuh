@@ -68,18 +68,23 @@ inline bool size_ok(long long rows, long long ld) {
 
 // ---- device: element helpers ----
 
-__device__ __forceinline__ float sigmoid(float x) {
-  return __fdividef(1.f, 1.f + __expf(-x));
-}
-// x sigmoid(x): -0 for x far below zero (1 + e^-x = inf), NaN for -inf as the
-// formula gives.
-__device__ __forceinline__ float silu(float x) { return __fdividef(x, 1.f + __expf(-x)); }
-
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+__device__ __forceinline__ float rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ float sigmoid(float x) {
+  return rcp(1.f + ex2(x * -1.4426950408889634f));
+}
+// x sigmoid(x): -0 for x far below zero (1 + e^-x = inf), NaN for -inf as the
+// formula gives.
+__device__ __forceinline__ float silu(float x) { return x * sigmoid(x); }
 
 // log(1 + e^x) = max(x, 0) + log(1 + e), e = e^-|x|, without overflow or
 // cancellation on either side.  log(1 + e) = 2 atanh(s), s = e / (2 + e) in
@@ -88,7 +93,7 @@ __device__ __forceinline__ float ex2(float x) {
 // general log1p, and as exact for tiny e.
 __device__ __forceinline__ float softplus(float x) {
   const float e = ex2(fabsf(x) * -1.4426950408889634f);
-  const float s = __fdividef(e, 2.f + e), q = s * s;
+  const float s = e * rcp(2.f + e), q = s * s;
   float r = fmaf(q, 0.28178334f, 0.27960601f);
   r = fmaf(q, r, 0.40024909f);
   r = fmaf(q, r, 0.66666317f);
@@ -169,6 +174,12 @@ struct Raw4<float> {
   float4 r;
   __device__ __forceinline__ float4 get() const { return r; }
 };
+template <typename T>
+__device__ __forceinline__ Raw4<T> ld_raw4(const T* p) {
+  Raw4<T> v;
+  v.r = *reinterpret_cast<const decltype(v.r)*>(p);
+  return v;
+}
 // The first n of the four at p (ld4's rule), zeros behind.
 template <typename T>
 __device__ __forceinline__ Raw4<T> ld_raw4(const T* p, int n, bool vec) {

@@ -109,11 +109,12 @@ scan_kernel(Args p) {
   static_assert(!REV || MODE == LOCAL, "only end states run backward");
   constexpr bool USE_B = !REV, USE_C = MODE == FULL || REV;
   extern __shared__ __align__(16) unsigned char smem_raw[];
-  // [2][TK][CH] (dt', dt' u) or (dt', g); [2][TK][N] B and C; [2][TK][CH] y
-  float2* s_x = reinterpret_cast<float2*>(smem_raw);
-  float* s_b = reinterpret_cast<float*>(s_x + 2 * TK * CH);
+  // [2][TK][CH] dt', then x = dt' u (or g), then y; [2][TK][N] B and C
+  float* s_d = reinterpret_cast<float*>(smem_raw);
+  float* s_x = s_d + 2 * TK * CH;
+  float* s_y = s_x + 2 * TK * CH;
+  float* s_b = s_y + (MODE == FULL ? 2 * TK * CH : 0);
   float* s_c = s_b + 2 * TK * N;
-  float* s_y = s_c + 2 * TK * N;
 
   const int Dg = p.D / p.G, TPG = (Dg + CH - 1) / CH;
   const int tiles = TPG * p.G;
@@ -155,15 +156,30 @@ scan_kernel(Args p) {
 
     Raw4<T> xn[IX], dn[IX], zn[IX], bn[IB], cn[IB];  // the tile to be staged next
     Raw4<T> xc[IX], zc[IX], xp[IX], zp[IX];          // u, z of the tiles in the scan and done
+    // tiles of tokens that all exist take no care of ends
+    const bool whole = vs && vdt && (vz || !has_z) && m >= 4;
     auto load = [&](int k) {
       const int t0 = t_lo + k * TK;
+      if (whole && t0 + TK <= t_live) {
+        const long long t = t0 + tt0;
+        const T *px = src + t * lds, *pd = dt + t * p.lddt, *pz = z + (has_z ? t * p.ldz : 0);
+        const long long sx = TS * lds, sd = TS * p.lddt, sz = TS * p.ldz;
 #pragma unroll
-      for (int i = 0; i < IX; ++i) {
-        const int t = t0 + tt0 + i * TS;
-        const int n = t < t_live ? m : 0;
-        xn[i] = ld_raw4(src + (long long)t * lds, n, vs);
-        dn[i] = ld_raw4(dt + (long long)t * p.lddt, n, vdt);
-        if (has_z) zn[i] = ld_raw4(z + (long long)t * p.ldz, n, vz);
+        for (int i = 0; i < IX; ++i) {
+          xn[i] = ld_raw4(px);
+          dn[i] = ld_raw4(pd);
+          if (has_z) zn[i] = ld_raw4(pz);
+          px += sx; pd += sd; pz += sz;
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < IX; ++i) {
+          const int t = t0 + tt0 + i * TS;
+          const int n = t < t_live ? m : 0;
+          xn[i] = ld_raw4(src + (long long)t * lds, n, vs);
+          dn[i] = ld_raw4(dt + (long long)t * p.lddt, n, vdt);
+          if (has_z) zn[i] = ld_raw4(z + (long long)t * p.ldz, n, vz);
+        }
       }
 #pragma unroll
       for (int i = 0; i < IB; ++i) {
@@ -175,7 +191,9 @@ scan_kernel(Args p) {
     };
     auto stage = [&](int k) {
       const int t0 = t_lo + k * TK;
-      float2* sx = s_x + (k & 1) * TK * CH;
+      float* sd = s_d + (k & 1) * TK * CH;
+      float* sx = s_x + (k & 1) * TK * CH;
+      const bool ends = m < 4 || t0 + TK > t_live;
 #pragma unroll
       for (int i = 0; i < IX; ++i) {
         const int tt = tt0 + i * TS;
@@ -186,12 +204,12 @@ scan_kernel(Args p) {
         }
         // tokens that do not exist, and channels past the last, step by 0:
         // their state stays as it is
-        const int n = t0 + tt < t_live ? m : 0;
-        if (n < 4) {
+        if (ends) {
+          const int n = t0 + tt < t_live ? m : 0;
           if (n < 1) d.x = 0.f;
           if (n < 2) d.y = 0.f;
           if (n < 3) d.z = 0.f;
-          d.w = 0.f;
+          if (n < 4) d.w = 0.f;
         }
         if (REV) {
           if (has_z) {
@@ -201,9 +219,8 @@ scan_kernel(Args p) {
         } else {
           x.x *= d.x; x.y *= d.y; x.z *= d.z; x.w *= d.w;
         }
-        float4* o = reinterpret_cast<float4*>(sx + tt * CH + c);
-        o[0] = make_float4(d.x, x.x, d.y, x.y);
-        o[1] = make_float4(d.z, x.z, d.w, x.w);
+        *reinterpret_cast<float4*>(sd + tt * CH + c) = d;
+        *reinterpret_cast<float4*>(sx + tt * CH + c) = x;
       }
 #pragma unroll
       for (int i = 0; i < IB; ++i) {
@@ -217,6 +234,23 @@ scan_kernel(Args p) {
     auto finish = [&](int k, const Raw4<T>(&xs)[IX], const Raw4<T>(&zs)[IX]) {
       const int t0 = t_lo + k * TK;
       const float* sy = s_y + (k & 1) * TK * CH;
+      if (vec && m >= 4 && t0 + TK <= t_live) {
+        T* py = y + (long long)(t0 + tt0) * p.D;
+#pragma unroll
+        for (int i = 0; i < IX; ++i) {
+          const float4 q = xs[i].get();
+          float4 v = *reinterpret_cast<const float4*>(sy + (tt0 + i * TS) * CH + c);
+          v.x = fmaf(skip.x, q.x, v.x); v.y = fmaf(skip.y, q.y, v.y);
+          v.z = fmaf(skip.z, q.z, v.z); v.w = fmaf(skip.w, q.w, v.w);
+          if (has_z) {
+            const float4 w = zs[i].get();
+            v.x *= silu(w.x); v.y *= silu(w.y); v.z *= silu(w.z); v.w *= silu(w.w);
+          }
+          IO<T>::st4(py, v);
+          py += (long long)TS * p.D;
+        }
+        return;
+      }
 #pragma unroll
       for (int i = 0; i < IX; ++i) {
         const int tt = tt0 + i * TS, t = t0 + tt;
@@ -297,7 +331,8 @@ scan_kernel(Args p) {
       }
   };
   auto scan = [&](int k) {
-    const float2* sx = s_x + (k & 1) * TK * CH + cc;
+    const float* sd = s_d + (k & 1) * TK * CH + cc;
+    const float* sx = s_x + (k & 1) * TK * CH + cc;
     const float* sb = s_b + (k & 1) * TK * N + nl * 4;
     const float* sc = s_c + (k & 1) * TK * N + nl * 4;
     float* sy = s_y + (k & 1) * TK * CH + cc;
@@ -322,17 +357,19 @@ scan_kernel(Args p) {
           const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(sc + t * N);
           cv[0] = v.x; cv[1] = v.y;
         }
-        float2 x[CPT];
+        float d[CPT], x[CPT];
         if constexpr (CPT == 2) {
-          const float4 v = *reinterpret_cast<const float4*>(sx + t * CH);
-          x[0] = make_float2(v.x, v.y);
-          x[1] = make_float2(v.z, v.w);
+          const float2 v = *reinterpret_cast<const float2*>(sd + t * CH);
+          const float2 w = *reinterpret_cast<const float2*>(sx + t * CH);
+          d[0] = v.x; d[1] = v.y;
+          x[0] = w.x; x[1] = w.y;
         } else {
+          d[0] = sd[t * CH];
           x[0] = sx[t * CH];
         }
 #pragma unroll
         for (int c = 0; c < CPT; ++c) {
-          const f32x2 d2 = pack2(x[c].x, x[c].x), w2 = pack2(x[c].y, x[c].y);
+          const f32x2 d2 = pack2(d[c], d[c]), w2 = pack2(x[c], x[c]);
           const f32x2 e0 = ex2_2(mul2(d2, a2[c][0])), e1 = ex2_2(mul2(d2, a2[c][1]));
           if (REV) {
             h[c][0] = mul2(e0, fma2(w2, cv[0], h[c][0]));
@@ -341,7 +378,7 @@ scan_kernel(Args p) {
             h[c][0] = fma2(e0, h[c][0], mul2(w2, bv[0]));
             h[c][1] = fma2(e1, h[c][1], mul2(w2, bv[1]));
           }
-          if (MODE == LOCAL) sum[c] += x[c].x;
+          if (MODE == LOCAL) sum[c] += d[c];
           if (MODE == FULL) {
             const float2 s = unpack2(fma2(cv[1], h[c][1], mul2(cv[0], h[c][0])));
             yv[i][c] = s.x + s.y;
