@@ -32,16 +32,20 @@ using namespace layer;
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kTile = 32;     // segments are multiples of this many tokens
-constexpr int kCW = 4;        // warps that run the recurrence
 constexpr int kCkpt = 16;     // tokens between the backward's saved states
 
 enum Mode { FULL = 0, LOCAL = 1, CKPT = 2 };
 
 template <int N>
 struct Shape {
-  static constexpr int LPC = N / 4;                  // lanes of a channel
-  static constexpr int CPT = N == 8 ? 1 : 2;         // channels of a thread
-  static constexpr int CH = kCW * (32 / LPC) * CPT;  // channels of a block
+  static constexpr int LPC = N / 4;            // lanes of a channel
+  static constexpr int CPT = 2;               // channels of a thread
+  static constexpr int CW = N == 8 ? 2 : 4;    // warps that run the recurrence
+  static constexpr int HW = 4;                 // helper warps
+  static constexpr int CPW = (32 / LPC) * CPT; // channels of a warp
+  static constexpr int CH = CW * CPW;          // channels of a block
+  static constexpr int NT = (CW + HW) * 32;
+  static constexpr int UN = LPC > 8 ? LPC : 8; // tokens in flight in the recurrence
 };
 
 // Tokens of a tile of the forward scan: what a helper thread's registers hold
@@ -97,12 +101,12 @@ __device__ __forceinline__ float step_of(float raw, bool sp) { return sp ? softp
 // (a tile's time covers the latency), and holds u and z until the tile's y is
 // there.
 template <typename T, int N, int MODE, bool REV>
-__global__ void __launch_bounds__(2 * kCW * 32, 2)
+__global__ void __launch_bounds__(Shape<N>::NT, 2)
 scan_kernel(Args p) {
   constexpr int LPC = Shape<N>::LPC, CPT = Shape<N>::CPT, CH = Shape<N>::CH;
   constexpr int TK = Tile<T, N>::TK;
-  constexpr int CPW = CH / kCW;  // channels of a warp
-  constexpr int NH = kCW * 32;   // helper threads
+  constexpr int CW = Shape<N>::CW, CPW = Shape<N>::CPW;
+  constexpr int NH = Shape<N>::HW * 32;  // helper threads
   constexpr int IX = TK * CH / 4 / NH;                      // channel groups of a helper
   constexpr int IB = (TK * N / 4 + NH - 1) / NH;            // groups of B and of C
   static_assert(IX * NH * 4 == TK * CH && NH % (CH / 4) == 0, "helpers share a tile evenly");
@@ -120,7 +124,9 @@ scan_kernel(Args p) {
   const int tiles = TPG * p.G;
   const int ct = blockIdx.x % tiles;
   const int rest = blockIdx.x / tiles;
-  const int sg = rest % p.S, b = rest / p.S;
+  // nobody starts from the end of the chain's last segment
+  const int ns = MODE == LOCAL ? p.S - 1 : p.S;
+  const int sg = rest % ns + (REV ? 1 : 0), b = rest / ns;
   const int g = ct / TPG;
   const int c0 = g * Dg + (ct % TPG) * CH;       // first channel
   const int nc = min(CH, (g + 1) * Dg - c0);     // channels that exist
@@ -131,9 +137,9 @@ scan_kernel(Args p) {
   const int first = REV ? ntile - 1 : 0, dir = REV ? -1 : 1;
   const long long row0 = (long long)b * p.T;
 
-  if (warp >= kCW) {
+  if (warp >= CW) {
     // ------------------------------------------------ helpers
-    const int hid = tid - NH;
+    const int hid = tid - CW * 32;
     const int c = (hid % (CH / 4)) * 4, tt0 = hid / (CH / 4);
     constexpr int TS = NH / (CH / 4);  // tokens between a helper's groups
     const int m = nc - c;              // channels that exist of this thread's four
@@ -336,7 +342,7 @@ scan_kernel(Args p) {
     const float* sb = s_b + (k & 1) * TK * N + nl * 4;
     const float* sc = s_c + (k & 1) * TK * N + nl * 4;
     float* sy = s_y + (k & 1) * TK * CH + cc;
-    constexpr int UN = MODE == FULL ? (LPC > 4 ? LPC : 4) : 4;
+    constexpr int UN = Shape<N>::UN;
 #pragma unroll 1
     for (int tt = 0; tt < TK; tt += UN) {
       if (MODE == CKPT && tt % kCkpt == 0) {
@@ -358,7 +364,12 @@ scan_kernel(Args p) {
           cv[0] = v.x; cv[1] = v.y;
         }
         float d[CPT], x[CPT];
-        if constexpr (CPT == 2) {
+        if constexpr (CPT == 4) {
+          const float4 v = *reinterpret_cast<const float4*>(sd + t * CH);
+          const float4 w = *reinterpret_cast<const float4*>(sx + t * CH);
+          d[0] = v.x; d[1] = v.y; d[2] = v.z; d[3] = v.w;
+          x[0] = w.x; x[1] = w.y; x[2] = w.z; x[3] = w.w;
+        } else if constexpr (CPT == 2) {
           const float2 v = *reinterpret_cast<const float2*>(sd + t * CH);
           const float2 w = *reinterpret_cast<const float2*>(sx + t * CH);
           d[0] = v.x; d[1] = v.y;
@@ -411,13 +422,11 @@ scan_kernel(Args p) {
 }
 
 // Chain over the segments: ends[b][s] (from a zero start) becomes the state
-// that segment s starts from; last gets the state behind the whole chain.
-// REV walks from the last segment to the first.
+// that segment s starts from.  REV walks from the last segment to the first.
 template <bool REV>
 __global__ void __launch_bounds__(256)
 chain_kernel(const float* __restrict__ A, const float* __restrict__ h0, float* __restrict__ ends,
-             const float* __restrict__ sums, float* __restrict__ last, int S, int D, int N,
-             long long total) {
+             const float* __restrict__ sums, int S, int D, int N, long long total) {
   const long long id = (long long)blockIdx.x * 256 + threadIdx.x;
   if (id >= total) return;
   const long long dn = (long long)D * N;
@@ -428,11 +437,14 @@ chain_kernel(const float* __restrict__ A, const float* __restrict__ h0, float* _
   for (int i = 0; i < S; ++i) {
     const int s = REV ? S - 1 - i : i;
     float* e = ends + (b * S + s) * dn + at;
+    if (i == S - 1) {
+      *e = h;
+      return;
+    }
     const float own = *e;
     *e = h;
     h = fmaf(ex2(a2 * sums[(b * S + s) * D + d]), h, own);
   }
-  if (last) last[id] = h;
 }
 
 // ---------------------------------------------------------------- backward
@@ -878,21 +890,21 @@ template <typename T, int N, int MODE, bool REV>
 static cudaError_t run_scan(const Args& a, cudaStream_t st) {
   constexpr int CH = Shape<N>::CH;
   const size_t smem = 2 * Tile<T, N>::TK * (CH * (8 + (MODE == FULL ? 4 : 0)) + 2 * N * 4);
-  const long long blocks = tiles_of(a.D, a.G, CH) * a.B * a.S;
+  const long long blocks = tiles_of(a.D, a.G, CH) * a.B * (MODE == LOCAL ? a.S - 1 : a.S);
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
   auto k = scan_kernel<T, N, MODE, REV>;
   cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  k<<<(unsigned)blocks, 2 * kCW * 32, smem, st>>>(a);
+  k<<<(unsigned)blocks, Shape<N>::NT, smem, st>>>(a);
   return cudaGetLastError();
 }
 
 template <bool REV>
-static cudaError_t run_chain(const Args& a, int N, const float* h0, float* last, cudaStream_t st) {
+static cudaError_t run_chain(const Args& a, int N, const float* h0, cudaStream_t st) {
   const long long total = (long long)a.B * a.D * N;
   if ((total + 255) / 256 > 0x7fffffffLL) return cudaErrorInvalidValue;
   chain_kernel<REV><<<(unsigned)((total + 255) / 256), 256, 0, st>>>(a.A, h0, a.ends, a.sums,
-                                                                     last, a.S, a.D, N, total);
+                                                                     a.S, a.D, N, total);
   return cudaGetLastError();
 }
 
@@ -900,7 +912,7 @@ template <typename T, int N, int MODE>
 static cudaError_t run_forward(const Args& a, cudaStream_t st) {
   if (a.S > 1) {
     cudaError_t e = run_scan<T, N, LOCAL, false>(a, st);
-    if (e == cudaSuccess) e = run_chain<false>(a, N, a.h0, nullptr, st);
+    if (e == cudaSuccess) e = run_chain<false>(a, N, a.h0, st);
     if (e != cudaSuccess) return e;
   }
   return run_scan<T, N, MODE, false>(a, st);
@@ -951,7 +963,7 @@ static cudaError_t run_backward(BwdArgs q, const BwdPlan& w, unsigned char* ws, 
   q.part_d = (float*)(ws + w.pd);
   if (w.r.S > 1) {
     e = run_scan<T, N, LOCAL, true>(q.f, st);
-    if (e == cudaSuccess) e = run_chain<true>(q.f, N, q.ghT, nullptr, st);
+    if (e == cudaSuccess) e = run_chain<true>(q.f, N, q.ghT, st);
     if (e != cudaSuccess) return e;
   }
   constexpr int CH = BwdShape<N>::CH, K = kCkpt;
