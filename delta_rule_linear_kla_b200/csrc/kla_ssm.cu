@@ -32,8 +32,10 @@ using namespace layer;
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kTile = 32;     // segments are multiples of this many tokens
-constexpr int kCkpt = 16;     // tokens between the backward's saved states
+constexpr int kCkpt = 8;      // tokens between the backward's saved states, and of its tiles
 
+// FULL: y, hT.  LOCAL: end states of the segments from zero starts.  CKPT: those
+// and the states on the way.
 enum Mode { FULL = 0, LOCAL = 1, CKPT = 2 };
 
 template <int N>
@@ -64,7 +66,9 @@ struct Args {
   float* hT;
   float* ends;   // [B][S][D][N] local end states, then start states
   float* sums;   // [B][S][D] sums of dt' of a segment
-  float* ckpt;   // [B][ceil(T/kCkpt)][D][N] states before every kCkpt-th token
+  // before every kCkpt-th token, with the sequence's ceil(T/kCkpt) side by side:
+  float* ckpt;   // [D][N] state, from a zero start of the segment where S > 1
+  float* cums;   // [D] sum of dt' since the segment's start (S > 1)
   int B, T, D, G, S, seg;  // seg: tokens of a segment, a multiple of kTile
   int softplus;
   // whether four elements of a row of each can be accessed at once
@@ -316,7 +320,7 @@ scan_kernel(Args p) {
       const float* from = nullptr;
       if (MODE != LOCAL) {
         if (p.S > 1)
-          from = p.ends + ((long long)b * p.S + sg) * p.D * N + at;
+          from = MODE == FULL ? p.ends + ((long long)b * p.S + sg) * p.D * N + at : nullptr;
         else if (p.h0)
           from = p.h0 + (long long)b * p.D * N + at;
       }
@@ -342,13 +346,21 @@ scan_kernel(Args p) {
     const float* sb = s_b + (k & 1) * TK * N + nl * 4;
     const float* sc = s_c + (k & 1) * TK * N + nl * 4;
     float* sy = s_y + (k & 1) * TK * CH + cc;
-    constexpr int UN = Shape<N>::UN;
+    constexpr int UN = MODE == FULL ? Shape<N>::UN : kCkpt;
+    static_assert(MODE != CKPT || UN == kCkpt, "a state is saved before every group");
 #pragma unroll 1
     for (int tt = 0; tt < TK; tt += UN) {
-      if (MODE == CKPT && tt % kCkpt == 0) {
+      if (MODE == CKPT) {
         const int t = t_lo + k * TK + tt;
-        if (t < t_hi)
-          save(p.ckpt + ((long long)b * ((p.T + kCkpt - 1) / kCkpt) + t / kCkpt) * p.D * N);
+        const long long at = (long long)b * ((p.T + kCkpt - 1) / kCkpt) + t / kCkpt;
+        if (t < t_hi) {
+          save(p.ckpt + at * p.D * N);
+          if (p.S > 1 && nl == 0) {
+#pragma unroll
+            for (int c = 0; c < CPT; ++c)
+              if (cc + c < nc) p.cums[at * p.D + c0 + cc + c] = sum[c];
+          }
+        }
       }
       float yv[UN][CPT];
 #pragma unroll
@@ -389,7 +401,7 @@ scan_kernel(Args p) {
             h[c][0] = fma2(e0, h[c][0], mul2(w2, bv[0]));
             h[c][1] = fma2(e1, h[c][1], mul2(w2, bv[1]));
           }
-          if (MODE == LOCAL) sum[c] += d[c];
+          if (MODE != FULL) sum[c] += d[c];
           if (MODE == FULL) {
             const float2 s = unpack2(fma2(cv[1], h[c][1], mul2(cv[0], h[c][0])));
             yv[i][c] = s.x + s.y;
@@ -412,7 +424,7 @@ scan_kernel(Args p) {
     scan(first + dir * i);
     __syncthreads();
   }
-  if (MODE == LOCAL) {
+  if (MODE == LOCAL || (MODE == CKPT && p.S > 1)) {
     save(p.ends + ((long long)b * p.S + sg) * p.D * N);
 #pragma unroll
     for (int c = 0; c < CPT; ++c)
@@ -453,44 +465,100 @@ chain_kernel(const float* __restrict__ A, const float* __restrict__ h0, float* _
 //   dh = e + C g;  dC = sum_d h g;  dB = sum_d dh dt' u;  e <- a dh
 //   du = D g + dt' sum_n dh B;  ddt' = u sum_n dh B + sum_n A h[t-1] e
 //   dA = sum_t dt' h[t-1] e;  dz = gy y0 silu'(z);  dD = sum g u
-// A block takes kCkpt tokens at a time from the segment's end: a thread
-// rebuilds the kCkpt states of its 4 from the saved one (decays and states
-// stay in registers), then walks back.  Sums over n cross the lanes of a
-// channel, sums over channels the other lanes and then the warps through
-// shared memory; dB and dC leave as one part a channel tile, dA, dD and
-// dt_bias as one part a segment, and reduce kernels add the parts in order:
-// no atomics, the same bits every time.
-constexpr int kBW = 8;  // warps of a backward block
+// Three passes: the states before every 8th token (scan_kernel, CKPT), the
+// adjoint states between segments where the sequence is cut (LOCAL, REV), and
+// bwd_kernel, which goes back through each segment 8 tokens at a time.
+//
+// bwd_kernel is split like the scan: recurrence warps with 4 states of 2
+// channels a thread (pairs of states packed), helper warps for everything that
+// is one value a channel.  A recurrence thread rebuilds 4 tokens' decays and
+// states in registers from the saved state (the first 4 of the 8 twice) and
+// walks them back.  Sums over n cross the lanes of a channel with 4 tokens
+// exchanged at once.  Sums over channels (dB, dC) cross the other lanes: there
+// register s of a thread holds state s ^ (its place among the channels), from
+// copies of B and C in that order, so that every exchange sends fixed
+// registers and needs no selection.  What bounds it are issue slots (about 140
+// instructions a token for 8 states) and the shared-memory pipe, which these
+// choices lighten.
+// dB and dC leave as one part a channel tile, dA, dD and dt_bias as one a
+// segment, and reduce kernels add the parts in order: no atomics, the same
+// bits every time.
 
 template <int N>
 struct BwdShape {
-  static constexpr int LPC = N / 4;
-  static constexpr int CPW = 32 / LPC;    // channels of a warp
-  static constexpr int CH = kBW * CPW;    // channels of a block
+  static constexpr int LPC = N / 4;              // lanes of a channel
+  static constexpr int CL = 32 / LPC;            // channel places of a warp
+  static constexpr int PB = CL < 4 ? CL : 4;     // orders of 4 states
+  static constexpr int CW = N == 8 ? 2 : 4;      // recurrence warps
+  static constexpr int HW = 2;                   // helper warps
+  static constexpr int CPW = 2 * CL;             // channels of a warp
+  static constexpr int CH = CW * CPW;            // channels of a block
+  static constexpr int NT = (CW + HW) * 32;
+  // shared memory of one buffer, in floats: dt', x, g; the three sums; B and
+  // C in every order; the warps' dB and dC
+  static constexpr int XS = kCkpt * CH;
+  static constexpr int BS = kCkpt * PB * N;
+  static constexpr int PS = CW * kCkpt * 2 * N;
+  static constexpr int BUF = 6 * XS + 2 * BS + PS;
 };
 
 struct BwdArgs {
-  Args f;                       // forward arguments; f.ckpt, f.ends = adjoint starts
+  Args f;                       // forward arguments; S, seg, ends, sums of the adjoint
+  int fS, fseg;                 // the forward's segments
+  const float* fends;           // [B][fS][D][N] their start states
   const float* ghT;
   void *du, *ddt, *dz;
-  float *dh0;
+  float* dh0;
   float* part_bc;               // [TPG][B][T][G][2N]
   float* part_a;                // [B*S][D][N]
   float* part_d;                // [B*S][2][D]: dD, ddt_bias
 };
 
+// v[j], j < 4: lane nl ends with the sum over the LPC lanes of a channel of
+// token (nl & 3) (LPC >= 4: in v[0]) or of tokens nl, nl + 2 (LPC = 2).
+template <int LPC>
+__device__ __forceinline__ void token_sums(float (&v)[4], int nl) {
+  if constexpr (LPC == 2) {
+#pragma unroll
+    for (int j = 0; j < 4; j += 2) {  // tokens j, j + 1
+      const float keep = (nl & 1) ? v[j + 1] : v[j], send = (nl & 1) ? v[j] : v[j + 1];
+      v[j] = keep + __shfl_xor_sync(0xffffffffu, send, 1);
+    }
+  } else {
+#pragma unroll
+    for (int off = LPC / 2; off >= 4; off >>= 1)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] += __shfl_xor_sync(0xffffffffu, v[j], off);
+    const bool up = (nl & 2) != 0;
+    const float k0 = up ? v[2] : v[0], s0 = up ? v[0] : v[2];
+    const float k1 = up ? v[3] : v[1], s1 = up ? v[1] : v[3];
+    v[0] = k0 + __shfl_xor_sync(0xffffffffu, s0, 2);
+    v[1] = k1 + __shfl_xor_sync(0xffffffffu, s1, 2);
+    const float k = (nl & 1) ? v[1] : v[0], s = (nl & 1) ? v[0] : v[1];
+    v[0] = k + __shfl_xor_sync(0xffffffffu, s, 1);
+  }
+}
+
+// (v.x, v.y, v.z, v.w) with register s holding component s ^ o; its own inverse.
+__device__ __forceinline__ float4 reorder(float4 v, int o) {
+  if (o & 1) v = make_float4(v.y, v.x, v.w, v.z);
+  if (o & 2) v = make_float4(v.z, v.w, v.x, v.y);
+  return v;
+}
+
 template <typename T, int N>
-__global__ void __launch_bounds__(kBW * 32, 1)
+__global__ void __launch_bounds__(BwdShape<N>::NT, 2)
 bwd_kernel(BwdArgs q) {
-  constexpr int LPC = BwdShape<N>::LPC, CPW = BwdShape<N>::CPW, CH = BwdShape<N>::CH;
-  constexpr int K = kCkpt;
+  using Sh = BwdShape<N>;
+  constexpr int LPC = Sh::LPC, CL = Sh::CL, PB = Sh::PB, CW = Sh::CW, CPW = Sh::CPW;
+  constexpr int CH = Sh::CH, K = kCkpt, NH = Sh::HW * 32;
+  constexpr int XG = K * CH / 4;                   // channel groups of a tile
+  constexpr int IX = (XG + NH - 1) / NH;           // of a helper
+  constexpr int IB = (K * N / 4 + NH - 1) / NH;
+  static_assert((XG % NH == 0 || XG < NH) && NH % (CH / 4) == 0, "helpers share a tile evenly");
   const Args& p = q.f;
   extern __shared__ __align__(16) unsigned char smem_raw[];
-  float4* s_x = reinterpret_cast<float4*>(smem_raw);     // [K][CH] dt', dt' u, g, u
-  float* s_b = reinterpret_cast<float*>(s_x + K * CH);   // [K][N]
-  float* s_c = s_b + K * N;                              // [K][N]
-  float4* s_o = reinterpret_cast<float4*>(s_c + K * N);  // [K][CH] sum dh B, sum A h e, y0
-  float* s_bc = reinterpret_cast<float*>(s_o + K * CH);  // [kBW][K][2N]
+  float* const smem = reinterpret_cast<float*>(smem_raw);
 
   const int Dg = p.D / p.G, TPG = (Dg + CH - 1) / CH;
   const int tiles = TPG * p.G;
@@ -501,246 +569,366 @@ bwd_kernel(BwdArgs q) {
   const int c0 = g * Dg + (ct % TPG) * CH;
   const int nc = min(CH, (g + 1) * Dg - c0);
   const int t_lo = sg * p.seg, t_hi = min(p.T, t_lo + p.seg);
-  const int n_live = live_tokens(p.lengths, b, p.T);
+  const int t_live = min(t_hi, live_tokens(p.lengths, b, p.T));
+  const int ntile = (t_hi - t_lo + K - 1) / K;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int nl = lane % LPC, cg = lane / LPC, cl = warp * CPW + cg;
   const long long row0 = (long long)b * p.T;
-  const T* u = (const T*)p.u + c0;
-  const T* dt = (const T*)p.dt + c0;
-  const T* z = p.z ? (const T*)p.z + c0 : nullptr;
-  const T* gy = (const T*)p.gy + c0;
-  const T* Bm = (const T*)p.Bm + (long long)g * N;
-  const T* Cm = (const T*)p.Cm + (long long)g * N;
-  const bool vec = (Dg & 3) == 0, vy = vec;
-  const bool vu = vec && p.vu, vdt = vec && p.vdt, vz = vec && p.vz, vb = p.vb, vc = p.vc;
-
-  const long long at = (long long)(c0 + cl) * N + nl * 4;
-  const bool mine = cl < nc;
-  float A[4] = {}, e[4] = {}, dA[4] = {};
-  if (mine) {
-    const float4 v = *reinterpret_cast<const float4*>(p.A + at);
-    A[0] = v.x; A[1] = v.y; A[2] = v.z; A[3] = v.w;
-    const float* from = p.S > 1 ? p.ends + ((long long)b * p.S + sg) * p.D * N + at
-                        : q.ghT ? q.ghT + (long long)b * p.D * N + at
-                                : nullptr;
-    if (from) {
-      const float4 w = *reinterpret_cast<const float4*>(from);
-      e[0] = w.x; e[1] = w.y; e[2] = w.z; e[3] = w.w;
-    }
-  }
-  // the 4 channels whose sums this thread keeps in the block's last step
-  constexpr int VPT = K * CH / 4 / (kBW * 32) > 0 ? K * CH / 4 / (kBW * 32) : 1;
-  static_assert((kBW * 32) % (CH / 4) == 0, "a thread keeps its channels");
-  float4 accD = make_float4(0.f, 0.f, 0.f, 0.f), accT = accD;
-
-  const int nchunk = (t_hi - t_lo + K - 1) / K;
-  const int nck = (p.T + K - 1) / K;
-  for (int ch = nchunk - 1; ch >= 0; --ch) {
-    const int t0 = t_lo + ch * K;
-    // inputs of the K tokens
-#pragma unroll
-    for (int v = 0; v < VPT; ++v) {
-      const int i = tid + v * kBW * 32;
-      if (i < K * CH / 4) {
-        const int tt = i / (CH / 4), c = (i % (CH / 4)) * 4, t = t0 + tt;
-        float4 d = make_float4(0.f, 0.f, 0.f, 0.f), x = d, gg = d;
-        if (t < t_hi && t < n_live && c < nc) {
-          const long long r = row0 + t;
-          const int m = nc - c;
-          d = ld4(dt + r * p.lddt + c, m, vdt);
-          if (p.bias) {
-            const float4 w = ld4(p.bias + c0 + c, m, vec);
-            d.x += w.x; d.y += w.y; d.z += w.z; d.w += w.w;
-          }
-          d.x = step_of(d.x, p.softplus); d.y = step_of(d.y, p.softplus);
-          d.z = step_of(d.z, p.softplus); d.w = step_of(d.w, p.softplus);
-          x = ld4(u + r * p.ldu + c, m, vu);
-          gg = ld4(gy + r * p.D + c, m, vy);
-          if (z) {
-            const float4 w = ld4(z + r * p.ldz + c, m, vz);
-            gg.x *= silu(w.x); gg.y *= silu(w.y); gg.z *= silu(w.z); gg.w *= silu(w.w);
-          }
-          if (m < 4) {
-            if (m < 2) d.y = x.y = gg.y = 0.f;
-            if (m < 3) d.z = x.z = gg.z = 0.f;
-            d.w = x.w = gg.w = 0.f;
-          }
-        }
-        float4* o = s_x + tt * CH + c;
-        o[0] = make_float4(d.x, d.x * x.x, gg.x, x.x);
-        o[1] = make_float4(d.y, d.y * x.y, gg.y, x.y);
-        o[2] = make_float4(d.z, d.z * x.z, gg.z, x.z);
-        o[3] = make_float4(d.w, d.w * x.w, gg.w, x.w);
-      }
-    }
-    for (int i = tid; i < K * N / 4; i += kBW * 32) {
-      const int tt = i / (N / 4), n = (i % (N / 4)) * 4, t = t0 + tt;
-      float4 b4 = make_float4(0.f, 0.f, 0.f, 0.f), c4 = b4;
-      if (t < t_hi && t < n_live) {
-        b4 = ld4(Bm + (row0 + t) * p.ldb + n, 4, vb);
-        c4 = ld4(Cm + (row0 + t) * p.ldc + n, 4, vc);
-      }
-      *reinterpret_cast<float4*>(s_b + tt * N + n) = b4;
-      *reinterpret_cast<float4*>(s_c + tt * N + n) = c4;
-    }
-    float h0[4] = {};
-    if (mine) {
-      const float4 v = *reinterpret_cast<const float4*>(
-          p.ckpt + ((long long)b * nck + t0 / K) * p.D * N + at);
-      h0[0] = v.x; h0[1] = v.y; h0[2] = v.z; h0[3] = v.w;
-    }
-    __syncthreads();
-    float a[K][4], h[K][4];
-#pragma unroll
-    for (int t = 0; t < K; ++t) {
-      const float4 x = s_x[t * CH + cl];
-      const float4 bv = *reinterpret_cast<const float4*>(s_b + t * N + nl * 4);
-      const float bb[4] = {bv.x, bv.y, bv.z, bv.w};
-      const float xd = x.x * kLog2e;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        a[t][i] = ex2(xd * A[i]);
-        h[t][i] = fmaf(a[t][i], t ? h[t > 0 ? t - 1 : 0][i] : h0[i], x.y * bb[i]);
-      }
-    }
-#pragma unroll
-    for (int t = K - 1; t >= 0; --t) {
-      const float4 x = s_x[t * CH + cl];
-      const float4 bv = *reinterpret_cast<const float4*>(s_b + t * N + nl * 4);
-      const float4 cv = *reinterpret_cast<const float4*>(s_c + t * N + nl * 4);
-      const float bb[4] = {bv.x, bv.y, bv.z, bv.w}, cv4[4] = {cv.x, cv.y, cv.z, cv.w};
-      float sB = 0.f, sA = 0.f, y0 = 0.f;
-      float w[8];  // dB, dC of 4 states, to be summed over the warp's channels
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float dh = fmaf(cv4[i], x.z, e[i]);
-        w[i] = dh * x.y;
-        w[4 + i] = h[t][i] * x.z;
-        y0 = fmaf(cv4[i], h[t][i], y0);
-        sB = fmaf(dh, bb[i], sB);
-        e[i] = a[t][i] * dh;
-        const float f = e[i] * (t ? h[t > 0 ? t - 1 : 0][i] : h0[i]);
-        sA = fmaf(A[i], f, sA);
-        dA[i] = fmaf(x.x, f, dA[i]);
-      }
-#pragma unroll
-      for (int off = LPC / 2; off > 0; off >>= 1) {
-        sB += __shfl_xor_sync(0xffffffffu, sB, off);
-        sA += __shfl_xor_sync(0xffffffffu, sA, off);
-        y0 += __shfl_xor_sync(0xffffffffu, y0, off);
-      }
-      if (nl == 0) s_o[t * CH + cl] = make_float4(sB, sA, y0, 0.f);
-      // over the CPW channels of the warp: halve the values a lane keeps
-      // while there are values to share, then add plainly
-      int keep = 8, first = 0;
-#pragma unroll
-      for (int off = CPW / 2; off > 0; off >>= 1) {
-        if (keep > 1) {
-          keep >>= 1;
-          const bool up = (cg & off) != 0;
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (i < keep) {
-              const float k0 = up ? w[i + keep] : w[i], s0 = up ? w[i] : w[i + keep];
-              w[i] = k0 + __shfl_xor_sync(0xffffffffu, s0, off * LPC);
-            }
-          first += up ? keep : 0;
-        } else {
-          w[0] += __shfl_xor_sync(0xffffffffu, w[0], off * LPC);
-        }
-      }
-      // value v of 8: dB (v < 4) or dC of state nl*4 + v % 4
-      float* o = s_bc + (warp * K + t) * 2 * N;
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (i < keep) {
-          const int v = first + i;
-          if (CPW <= 8 || (cg & 1) == 0)
-            o[(v >= 4 ? N : 0) + nl * 4 + (v & 3)] = w[i];
-        }
-    }
-    __syncthreads();
-    // dB, dC of the K tokens: the warps' sums in order
-    float* pbc = q.part_bc + (((long long)(ct % TPG) * p.B + b) * p.T * p.G + g) * 2 * N;
-    for (int i = tid; i < K * 2 * N; i += kBW * 32) {
-      const int tt = i / (2 * N), n = i % (2 * N);
-      if (t0 + tt < t_hi) {
-        float s = 0.f;
-#pragma unroll
-        for (int w = 0; w < kBW; ++w) s += s_bc[(w * K + tt) * 2 * N + n];
-        pbc[(long long)(t0 + tt) * p.G * 2 * N + n] = s;
-      }
-    }
-    // du, ddt, dz
-#pragma unroll
-    for (int v = 0; v < VPT; ++v) {
-      const int i = tid + v * kBW * 32;
-      if (i < K * CH / 4) {
-        const int tt = i / (CH / 4), c = (i % (CH / 4)) * 4, t = t0 + tt;
-        if (t < t_hi && c < nc) {
-          const long long r = row0 + t;
-          const int m = nc - c;
-          float4 vdu = make_float4(0.f, 0.f, 0.f, 0.f), vddt = vdu, vdz = vdu;
-          if (t < n_live) {
-            float4 raw = vdu, zz = vdu, g0 = vdu, dw = vdu;
-            if (p.softplus) {
-              raw = ld4(dt + r * p.lddt + c, m, vdt);
-              if (p.bias) {
-                const float4 w = ld4(p.bias + c0 + c, m, vec);
-                raw.x += w.x; raw.y += w.y; raw.z += w.z; raw.w += w.w;
-              }
-            }
-            if (p.Dw) dw = ld4(p.Dw + c0 + c, m, vec);
-            if (z) {
-              zz = ld4(z + r * p.ldz + c, m, vz);
-              g0 = ld4(gy + r * p.D + c, m, vy);
-            }
-            auto one = [&](int k, float rw, float zv, float gv, float dv, float& du, float& ddt,
-                           float& dzo, float& aD, float& aT) {
-              const float4 x = s_x[tt * CH + c + k], o = s_o[tt * CH + c + k];
-              du = fmaf(dv, x.z, o.x * x.x);
-              ddt = fmaf(o.x, x.w, o.y);
-              if (p.softplus) ddt *= sigmoid(rw);
-              if (z) {
-                const float s = sigmoid(zv);
-                dzo = gv * fmaf(dv, x.w, o.z) * (s * fmaf(zv, 1.f - s, 1.f));
-              }
-              aD = fmaf(x.z, x.w, aD);
-              aT += ddt;
-            };
-            one(0, raw.x, zz.x, g0.x, dw.x, vdu.x, vddt.x, vdz.x, accD.x, accT.x);
-            one(1, raw.y, zz.y, g0.y, dw.y, vdu.y, vddt.y, vdz.y, accD.y, accT.y);
-            one(2, raw.z, zz.z, g0.z, dw.z, vdu.z, vddt.z, vdz.z, accD.z, accT.z);
-            one(3, raw.w, zz.w, g0.w, dw.w, vdu.w, vddt.w, vdz.w, accD.w, accT.w);
-          }
-          st4((T*)q.du + c0 + r * p.D + c, vdu, m, vy);
-          st4((T*)q.ddt + c0 + r * p.D + c, vddt, m, vy);
-          if (z) st4((T*)q.dz + c0 + r * p.D + c, vdz, m, vy);
-        }
-      }
-    }
-    __syncthreads();
-  }
   const long long ps = (long long)b * p.S + sg;
-  if (mine) {
-    *reinterpret_cast<float4*>(q.part_a + ps * p.D * N + at) =
-        make_float4(dA[0], dA[1], dA[2], dA[3]);
-    if (q.dh0 && sg == 0)
-      *reinterpret_cast<float4*>(q.dh0 + (long long)b * p.D * N + at) =
-          make_float4(e[0], e[1], e[2], e[3]);
+
+  if (warp >= CW) {
+    // ------------------------------------------------ helpers
+    const int hid = tid - CW * 32;
+    const int c = (hid % (CH / 4)) * 4, tt0 = hid / (CH / 4);
+    constexpr int TS = NH / (CH / 4);
+    const int m = XG < NH && hid >= XG ? 0 : nc - c;
+    const bool vec = (Dg & 3) == 0;
+    const bool vu = vec && p.vu, vdt = vec && p.vdt, vz = vec && p.vz;
+    const bool has_z = p.z != nullptr, sp = p.softplus != 0;
+    const T* u = (const T*)p.u + row0 * p.ldu + c0 + c;
+    const T* dt = (const T*)p.dt + row0 * p.lddt + c0 + c;
+    const T* gy = (const T*)p.gy + row0 * p.D + c0 + c;
+    const T* z = has_z ? (const T*)p.z + row0 * p.ldz + c0 + c : nullptr;
+    const T* Bm = (const T*)p.Bm + row0 * p.ldb + (long long)g * N;
+    const T* Cm = (const T*)p.Cm + row0 * p.ldc + (long long)g * N;
+    T* du = (T*)q.du + row0 * p.D + c0 + c;
+    T* ddt = (T*)q.ddt + row0 * p.D + c0 + c;
+    T* dz = has_z ? (T*)q.dz + row0 * p.D + c0 + c : nullptr;
+    float* pbc = q.part_bc + (((long long)(ct % TPG) * p.B + b) * p.T * p.G + g) * 2 * N;
+    float4 bias = make_float4(0.f, 0.f, 0.f, 0.f), skip = bias, accD = bias, accT = bias;
+    if (p.bias) bias = ld4(p.bias + c0 + c, m, vec);
+    if (p.Dw) skip = ld4(p.Dw + c0 + c, m, vec);
+
+    struct Rows {
+      Raw4<T> u[IX], dt[IX], gy[IX], z[IX];
+    };
+    Rows next, cur, done;  // to be staged, in the recurrence, finished
+    Raw4<T> bn[IB], cn[IB];
+    auto load = [&](int k) {
+      const int t0 = t_lo + k * K;
+#pragma unroll
+      for (int i = 0; i < IX; ++i) {
+        const int t = t0 + tt0 + i * TS;
+        const int n = t < t_live ? m : 0;
+        next.u[i] = ld_raw4(u + (long long)t * p.ldu, n, vu);
+        next.dt[i] = ld_raw4(dt + (long long)t * p.lddt, n, vdt);
+        next.gy[i] = ld_raw4(gy + (long long)t * p.D, n, vec);
+        if (has_z) next.z[i] = ld_raw4(z + (long long)t * p.ldz, n, vz);
+      }
+#pragma unroll
+      for (int i = 0; i < IB; ++i) {
+        const int j = hid + i * NH, t = t0 + j / (N / 4), n = (j % (N / 4)) * 4;
+        const int have = j < K * N / 4 && t < t_live ? 4 : 0;
+        bn[i] = ld_raw4(Bm + (long long)t * p.ldb + n, have, p.vb);
+        cn[i] = ld_raw4(Cm + (long long)t * p.ldc + n, have, p.vc);
+      }
+    };
+    auto stage = [&](int k) {
+      float* buf = smem + (k & 1) * Sh::BUF;
+      const int t0 = t_lo + k * K;
+#pragma unroll
+      for (int i = 0; i < IX; ++i) {
+        const int tt = tt0 + i * TS;
+        if (XG < NH && hid >= XG) continue;
+        float4 d = next.dt[i].get(), x = next.u[i].get(), gg = next.gy[i].get();
+        d.x += bias.x; d.y += bias.y; d.z += bias.z; d.w += bias.w;
+        if (sp) {
+          d.x = softplus(d.x); d.y = softplus(d.y); d.z = softplus(d.z); d.w = softplus(d.w);
+        }
+        const int n = t0 + tt < t_live ? m : 0;  // zero steps as in the scan
+        if (n < 1) d.x = 0.f;
+        if (n < 2) d.y = 0.f;
+        if (n < 3) d.z = 0.f;
+        if (n < 4) d.w = 0.f;
+        if (has_z) {
+          const float4 w = next.z[i].get();
+          gg.x *= silu(w.x); gg.y *= silu(w.y); gg.z *= silu(w.z); gg.w *= silu(w.w);
+        }
+        x.x *= d.x; x.y *= d.y; x.z *= d.z; x.w *= d.w;
+        float* o = buf + tt * CH + c;
+        *reinterpret_cast<float4*>(o) = d;
+        *reinterpret_cast<float4*>(o + Sh::XS) = x;
+        *reinterpret_cast<float4*>(o + 2 * Sh::XS) = gg;
+      }
+#pragma unroll
+      for (int i = 0; i < IB; ++i) {
+        const int j = hid + i * NH;
+        if (j < K * N / 4) {
+          float* o = buf + 6 * Sh::XS + (j / (N / 4)) * PB * N + (j % (N / 4)) * 4;
+#pragma unroll
+          for (int r = 0; r < PB; ++r) {
+            *reinterpret_cast<float4*>(o + r * N) = reorder(bn[i].get(), r);
+            *reinterpret_cast<float4*>(o + Sh::BS + r * N) = reorder(cn[i].get(), r);
+          }
+        }
+      }
+    };
+    auto finish = [&](int k) {
+      const float* buf = smem + (k & 1) * Sh::BUF;
+      const int t0 = t_lo + k * K;
+#pragma unroll
+      for (int i = 0; i < IX; ++i) {
+        const int tt = tt0 + i * TS, t = t0 + tt;
+        if (t >= t_hi || m <= 0) continue;
+        float4 vdu = make_float4(0.f, 0.f, 0.f, 0.f), vddt = vdu, vdz = vdu;
+        if (t < t_live) {
+          const float* o = buf + tt * CH + c;
+          const float4 d = *reinterpret_cast<const float4*>(o);
+          const float4 gg = *reinterpret_cast<const float4*>(o + 2 * Sh::XS);
+          const float4 sB = *reinterpret_cast<const float4*>(o + 3 * Sh::XS);
+          const float4 sA = *reinterpret_cast<const float4*>(o + 4 * Sh::XS);
+          const float4 y0 = *reinterpret_cast<const float4*>(o + 5 * Sh::XS);
+          const float4 uu = done.u[i].get(), raw = done.dt[i].get();
+          auto one = [&](float d, float gg, float sB, float sA, float uu, float raw, float skip,
+                         float& du, float& ddt, float& aD, float& aT) {
+            du = fmaf(skip, gg, sB * d);
+            // sA is the sum with A log2 e
+            ddt = fmaf(sB, uu, sA * 0.6931471805599453f);
+            if (sp) ddt *= sigmoid(raw);
+            aD = fmaf(gg, uu, aD);
+            aT += ddt;
+          };
+          one(d.x, gg.x, sB.x, sA.x, uu.x, raw.x + bias.x, skip.x, vdu.x, vddt.x, accD.x, accT.x);
+          one(d.y, gg.y, sB.y, sA.y, uu.y, raw.y + bias.y, skip.y, vdu.y, vddt.y, accD.y, accT.y);
+          one(d.z, gg.z, sB.z, sA.z, uu.z, raw.z + bias.z, skip.z, vdu.z, vddt.z, accD.z, accT.z);
+          one(d.w, gg.w, sB.w, sA.w, uu.w, raw.w + bias.w, skip.w, vdu.w, vddt.w, accD.w, accT.w);
+          if (has_z) {
+            const float4 zz = done.z[i].get(), g0 = done.gy[i].get();
+            auto gate = [&](float z, float g0, float y0, float skip, float uu) {
+              const float s = sigmoid(z);
+              return g0 * fmaf(skip, uu, y0) * (s * fmaf(z, 1.f - s, 1.f));
+            };
+            vdz = make_float4(gate(zz.x, g0.x, y0.x, skip.x, uu.x),
+                              gate(zz.y, g0.y, y0.y, skip.y, uu.y),
+                              gate(zz.z, g0.z, y0.z, skip.z, uu.z),
+                              gate(zz.w, g0.w, y0.w, skip.w, uu.w));
+          }
+        }
+        st4(du + (long long)t * p.D, vdu, m, vec);
+        st4(ddt + (long long)t * p.D, vddt, m, vec);
+        if (has_z) st4(dz + (long long)t * p.D, vdz, m, vec);
+      }
+      // dB, dC: the warps' sums in order
+      const float* bc = buf + 6 * Sh::XS + 2 * Sh::BS;
+#pragma unroll
+      for (int i = 0; i < K * 2 * N / 4; i += NH) {
+        const int j = (i + hid) * 4, tt = j / (2 * N), n = j % (2 * N);
+        if (i + hid < K * 2 * N / 4 && t0 + tt < t_hi) {
+          float4 v = *reinterpret_cast<const float4*>(bc + j);
+#pragma unroll
+          for (int w = 1; w < CW; ++w) {
+            const float4 a = *reinterpret_cast<const float4*>(bc + w * K * 2 * N + j);
+            v.x += a.x; v.y += a.y; v.z += a.z; v.w += a.w;
+          }
+          *reinterpret_cast<float4*>(pbc + (long long)(t0 + tt) * p.G * 2 * N + n) = v;
+        }
+      }
+    };
+    load(ntile - 1);
+    stage(ntile - 1);
+    cur = next;
+    if (ntile > 1) load(ntile - 2);
+    __syncthreads();
+    for (int k = ntile - 1; k >= 0; --k) {
+      if (k + 1 < ntile) finish(k + 1);  // before its buffer is filled anew
+      if (k > 0) stage(k - 1);
+      done = cur;
+      cur = next;
+      if (k > 1) load(k - 2);
+      __syncthreads();
+    }
+    finish(0);
+    // dD, ddt_bias: over the threads that kept the same 4 channels, through
+    // the other buffer
+    float* red = smem + Sh::BUF;
+    asm volatile("bar.sync 1, %0;" ::"n"(NH) : "memory");
+    *reinterpret_cast<float4*>(red + hid * 4) = accD;
+    *reinterpret_cast<float4*>(red + NH * 4 + hid * 4) = accT;
+    asm volatile("bar.sync 1, %0;" ::"n"(NH) : "memory");
+    for (int i = hid; i < 2 * CH; i += NH) {
+      const int w = i / CH, cc = i % CH;
+      if (cc < nc) {
+        float s = 0.f;
+        for (int r = cc / 4; r < NH; r += CH / 4) s += red[(w * NH + r) * 4 + (cc & 3)];
+        q.part_d[(ps * 2 + w) * p.D + c0 + cc] = s;
+      }
+    }
+    return;
   }
-  // dD, ddt_bias: over the threads that kept the same 4 channels
-  float4* red = s_x;  // [2][kBW * 32], free after the last barrier
-  red[tid] = accD;
-  red[kBW * 32 + tid] = accT;
+
+  // -------------------------------------------------- recurrence
+  const int nl = lane % LPC, cg = lane / LPC, cc = warp * CPW + cg * 2;
+  const int ord = cg & (PB - 1);  // register s holds state nl * 4 + (s ^ ord)
+  auto row = [&](const float* base, int k) {
+    if (!base || cc + k >= nc) return make_float4(0.f, 0.f, 0.f, 0.f);
+    return reorder(*reinterpret_cast<const float4*>(base + (long long)(c0 + cc + k) * N + nl * 4),
+                   ord);
+  };
+  f32x2 a2[2][2], e[2][2], dA[2][2];
+  const float* from = p.S > 1 ? p.ends + ps * p.D * N
+                      : q.ghT ? q.ghT + (long long)b * p.D * N
+                              : nullptr;
+#pragma unroll
+  for (int c = 0; c < 2; ++c) {
+    const float4 v = row(p.A, c), w = row(from, c);
+    a2[c][0] = pack2(v.x * kLog2e, v.y * kLog2e);
+    a2[c][1] = pack2(v.z * kLog2e, v.w * kLog2e);
+    e[c][0] = pack2(w.x, w.y);
+    e[c][1] = pack2(w.z, w.w);
+    dA[c][0] = dA[c][1] = pack2(0.f, 0.f);
+  }
+  const int nck = (p.T + K - 1) / K;
   __syncthreads();
-  for (int i = tid; i < 2 * CH; i += kBW * 32) {
-    const int w = i / CH, c = i % CH;
-    if (c < nc) {
-      float s = 0.f;
-      for (int r = c / 4; r < kBW * 32; r += CH / 4)
-        s += reinterpret_cast<const float*>(red + w * kBW * 32 + r)[c & 3];
-      q.part_d[(ps * 2 + w) * p.D + c0 + c] = s;
+  for (int k = ntile - 1; k >= 0; --k) {
+    float* buf = smem + (k & 1) * Sh::BUF;
+    const float* sd = buf + cc;
+    const float* sb = buf + 6 * Sh::XS + ord * N + nl * 4;
+    // the state before the tile's first token
+    f32x2 h0[2][2];
+    {
+      const int t = t_lo + k * K;
+      const long long ck = (long long)b * nck + t / K;
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const float4 v = row(p.ckpt + ck * p.D * N, c);
+        h0[c][0] = pack2(v.x, v.y);
+        h0[c][1] = pack2(v.z, v.w);
+        if (q.fS > 1) {  // saved from a zero start: add what the segment's start left
+          const float4 w = row(q.fends + ((long long)b * q.fS + t / q.fseg) * p.D * N, c);
+          const float s = cc + c < nc ? p.cums[ck * p.D + c0 + cc + c] : 0.f;
+          const f32x2 s2 = pack2(s, s);
+          h0[c][0] = fma2(ex2_2(mul2(s2, a2[c][0])), pack2(w.x, w.y), h0[c][0]);
+          h0[c][1] = fma2(ex2_2(mul2(s2, a2[c][1])), pack2(w.z, w.w), h0[c][1]);
+        }
+      }
+    }
+    f32x2 tA[2][2];
+    tA[0][0] = tA[0][1] = tA[1][0] = tA[1][1] = pack2(0.f, 0.f);
+    // one token forward: its decays, and h moved on
+    auto forward = [&](int t, f32x2 (&h)[2][2], f32x2 (&a)[2][2]) {
+      const float2 d = *reinterpret_cast<const float2*>(sd + t * CH);
+      const float2 x = *reinterpret_cast<const float2*>(sd + Sh::XS + t * CH);
+      const ulonglong2 bv = *reinterpret_cast<const ulonglong2*>(sb + t * PB * N);
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const f32x2 d2 = c ? pack2(d.y, d.y) : pack2(d.x, d.x);
+        const f32x2 x2 = c ? pack2(x.y, x.y) : pack2(x.x, x.x);
+        a[c][0] = ex2_2(mul2(d2, a2[c][0]));
+        a[c][1] = ex2_2(mul2(d2, a2[c][1]));
+        h[c][0] = fma2(a[c][0], h[c][0], mul2(x2, bv.x));
+        h[c][1] = fma2(a[c][1], h[c][1], mul2(x2, bv.y));
+      }
+    };
+    auto half = [&](int tb, const f32x2 (&hs)[2][2]) {
+      f32x2 a[4][2][2], h[5][2][2];
+#pragma unroll
+      for (int c = 0; c < 2; ++c) { h[0][c][0] = hs[c][0]; h[0][c][1] = hs[c][1]; }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+#pragma unroll
+        for (int c = 0; c < 2; ++c) { h[i + 1][c][0] = h[i][c][0]; h[i + 1][c][1] = h[i][c][1]; }
+        forward(tb + i, h[i + 1], a[i]);
+      }
+      float vB[2][4], vA[2][4], vY[2][4];
+#pragma unroll
+      for (int i = 3; i >= 0; --i) {
+        const int t = tb + i;
+        const float2 d = *reinterpret_cast<const float2*>(sd + t * CH);
+        const float2 x = *reinterpret_cast<const float2*>(sd + Sh::XS + t * CH);
+        const float2 gg = *reinterpret_cast<const float2*>(sd + 2 * Sh::XS + t * CH);
+        const ulonglong2 bv = *reinterpret_cast<const ulonglong2*>(sb + t * PB * N);
+        const ulonglong2 cv = *reinterpret_cast<const ulonglong2*>(sb + Sh::BS + t * PB * N);
+        f32x2 wB[2], wC[2];
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const f32x2 d2 = c ? pack2(d.y, d.y) : pack2(d.x, d.x);
+          const f32x2 x2 = c ? pack2(x.y, x.y) : pack2(x.x, x.x);
+          const f32x2 g2 = c ? pack2(gg.y, gg.y) : pack2(gg.x, gg.x);
+          const f32x2 dh0 = fma2(cv.x, g2, e[c][0]), dh1 = fma2(cv.y, g2, e[c][1]);
+          wB[0] = c ? fma2(dh0, x2, wB[0]) : mul2(dh0, x2);
+          wB[1] = c ? fma2(dh1, x2, wB[1]) : mul2(dh1, x2);
+          wC[0] = c ? fma2(h[i + 1][c][0], g2, wC[0]) : mul2(h[i + 1][c][0], g2);
+          wC[1] = c ? fma2(h[i + 1][c][1], g2, wC[1]) : mul2(h[i + 1][c][1], g2);
+          const float2 y = unpack2(fma2(cv.y, h[i + 1][c][1], mul2(cv.x, h[i + 1][c][0])));
+          vY[c][i] = y.x + y.y;
+          const float2 sB = unpack2(fma2(dh1, bv.y, mul2(dh0, bv.x)));
+          vB[c][i] = sB.x + sB.y;
+          e[c][0] = mul2(a[i][c][0], dh0);
+          e[c][1] = mul2(a[i][c][1], dh1);
+          const f32x2 f0 = mul2(e[c][0], h[i][c][0]), f1 = mul2(e[c][1], h[i][c][1]);
+          const float2 sA = unpack2(fma2(a2[c][1], f1, mul2(a2[c][0], f0)));
+          vA[c][i] = sA.x + sA.y;
+          tA[c][0] = fma2(d2, f0, tA[c][0]);
+          tA[c][1] = fma2(d2, f1, tA[c][1]);
+        }
+        // dB, dC over the warp's channels
+        const float2 b01 = unpack2(wB[0]), b23 = unpack2(wB[1]), c01 = unpack2(wC[0]),
+                     c23 = unpack2(wC[1]);
+        float rb0 = b01.x + __shfl_xor_sync(0xffffffffu, b01.y, LPC);
+        float rb2 = b23.x + __shfl_xor_sync(0xffffffffu, b23.y, LPC);
+        float rc0 = c01.x + __shfl_xor_sync(0xffffffffu, c01.y, LPC);
+        float rc2 = c23.x + __shfl_xor_sync(0xffffffffu, c23.y, LPC);
+        float* o = buf + 6 * Sh::XS + 2 * Sh::BS + (warp * K + t) * 2 * N + nl * 4;
+        if constexpr (CL == 2) {
+          o[ord] = rb0;
+          o[2 ^ ord] = rb2;
+          o[N + ord] = rc0;
+          o[N + (2 ^ ord)] = rc2;
+        } else {
+          rb0 += __shfl_xor_sync(0xffffffffu, rb2, 2 * LPC);
+          rc0 += __shfl_xor_sync(0xffffffffu, rc2, 2 * LPC);
+          if constexpr (CL == 4) {
+            o[ord] = rb0;
+            o[N + ord] = rc0;
+          } else {
+            const bool up = (cg & 4) != 0;
+            float v = up ? rc0 : rb0;
+            v += __shfl_xor_sync(0xffffffffu, up ? rb0 : rc0, 4 * LPC);
+            if constexpr (CL == 16) v += __shfl_xor_sync(0xffffffffu, v, 8 * LPC);
+            if (CL == 8 || cg < 8) o[(up ? N : 0) + ord] = v;
+          }
+        }
+      }
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        token_sums<LPC>(vB[c], nl);
+        token_sums<LPC>(vA[c], nl);
+        token_sums<LPC>(vY[c], nl);
+      }
+      if (LPC <= 4 || nl < 4) {
+#pragma unroll
+        for (int j = 0; j < (LPC == 2 ? 4 : 1); j += 2) {
+          float* o = buf + 3 * Sh::XS + (tb + j + nl) * CH + cc;
+          *reinterpret_cast<float2*>(o) = make_float2(vB[0][j], vB[1][j]);
+          *reinterpret_cast<float2*>(o + Sh::XS) = make_float2(vA[0][j], vA[1][j]);
+          *reinterpret_cast<float2*>(o + 2 * Sh::XS) = make_float2(vY[0][j], vY[1][j]);
+        }
+      }
+    };
+    f32x2 hm[2][2], skip_a[2][2];
+#pragma unroll
+    for (int c = 0; c < 2; ++c) { hm[c][0] = h0[c][0]; hm[c][1] = h0[c][1]; }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) forward(i, hm, skip_a);
+    half(4, hm);
+    half(0, h0);
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {  // per tile first: shorter chains of additions
+      dA[c][0] = add2(dA[c][0], tA[c][0]);
+      dA[c][1] = add2(dA[c][1], tA[c][1]);
+    }
+    __syncthreads();
+  }
+#pragma unroll
+  for (int c = 0; c < 2; ++c) {
+    if (cc + c >= nc) continue;
+    const long long at = (long long)(c0 + cc + c) * N + nl * 4;
+    const float2 v0 = unpack2(dA[c][0]), v1 = unpack2(dA[c][1]);
+    *reinterpret_cast<float4*>(q.part_a + ps * p.D * N + at) =
+        reorder(make_float4(v0.x, v0.y, v1.x, v1.y), ord);
+    if (q.dh0 && sg == 0) {
+      const float2 e0 = unpack2(e[c][0]), e1 = unpack2(e[c][1]);
+      *reinterpret_cast<float4*>(q.dh0 + (long long)b * p.D * N + at) =
+          reorder(make_float4(e0.x, e0.y, e1.x, e1.y), ord);
     }
   }
 }
@@ -908,20 +1096,20 @@ static cudaError_t run_chain(const Args& a, int N, const float* h0, cudaStream_t
   return cudaGetLastError();
 }
 
-template <typename T, int N, int MODE>
+template <typename T, int N>
 static cudaError_t run_forward(const Args& a, cudaStream_t st) {
   if (a.S > 1) {
     cudaError_t e = run_scan<T, N, LOCAL, false>(a, st);
     if (e == cudaSuccess) e = run_chain<false>(a, N, a.h0, st);
     if (e != cudaSuccess) return e;
   }
-  return run_scan<T, N, MODE, false>(a, st);
+  return run_scan<T, N, FULL, false>(a, st);
 }
 
 struct BwdPlan {
   Split f, r;
   int TPG;
-  size_t ckpt, fends, fsums, rends, rsums, bc, pa, pd, total;
+  size_t ckpt, cums, fends, fsums, rends, rsums, bc, pa, pd, total;
 };
 
 static BwdPlan bwd_plan(int B, int T, int D, int G, int N) {
@@ -929,10 +1117,11 @@ static BwdPlan bwd_plan(int B, int T, int D, int G, int N) {
   w.f = fwd_split(B, T, D, G, N);
   w.r = bwd_split(B, T, D, G, N);
   w.TPG = (D / G + bwd_channels(N) - 1) / bwd_channels(N);
-  const size_t dn = (size_t)D * N * 4;
+  const size_t dn = (size_t)D * N * 4, nck = (size_t)B * ((T + kCkpt - 1) / kCkpt);
   size_t at = 0;
   auto take = [&](size_t n) { size_t r = at; at += up(n); return r; };
-  w.ckpt = take((size_t)B * ((T + kCkpt - 1) / kCkpt) * dn);
+  w.ckpt = take(nck * dn);
+  w.cums = take(w.f.S > 1 ? nck * D * 4 : 0);
   w.fends = take(w.f.S > 1 ? B * w.f.S * dn : 0);
   w.fsums = take(w.f.S > 1 ? (size_t)B * w.f.S * D * 4 : 0);
   w.rends = take(w.r.S > 1 ? B * w.r.S * dn : 0);
@@ -949,12 +1138,15 @@ static cudaError_t run_backward(BwdArgs q, const BwdPlan& w, unsigned char* ws, 
                                 float* dD, float* dbias, void* dB, void* dC, cudaStream_t st) {
   Args f = q.f;
   f.ckpt = (float*)(ws + w.ckpt);
+  f.cums = (float*)(ws + w.cums);
   f.S = w.f.S; f.seg = w.f.seg;
   f.ends = (float*)(ws + w.fends);
   f.sums = (float*)(ws + w.fsums);
-  cudaError_t e = run_forward<T, N, CKPT>(f, st);
+  cudaError_t e = run_scan<T, N, CKPT, false>(f, st);
+  if (e == cudaSuccess && f.S > 1) e = run_chain<false>(f, N, f.h0, st);
   if (e != cudaSuccess) return e;
-  q.f.ckpt = f.ckpt;
+  q.fS = f.S; q.fseg = f.seg; q.fends = f.ends;
+  q.f.ckpt = f.ckpt; q.f.cums = f.cums;
   q.f.S = w.r.S; q.f.seg = w.r.seg;
   q.f.ends = (float*)(ws + w.rends);
   q.f.sums = (float*)(ws + w.rsums);
@@ -966,15 +1158,15 @@ static cudaError_t run_backward(BwdArgs q, const BwdPlan& w, unsigned char* ws, 
     if (e == cudaSuccess) e = run_chain<true>(q.f, N, q.ghT, st);
     if (e != cudaSuccess) return e;
   }
-  constexpr int CH = BwdShape<N>::CH, K = kCkpt;
-  size_t smem = (size_t)K * CH * 32 + K * N * 8 + (size_t)kBW * K * 2 * N * 4;
-  if (smem < 2 * kBW * 32 * 16) smem = 2 * kBW * 32 * 16;
-  const long long blocks = tiles_of(q.f.D, q.f.G, CH) * q.f.B * q.f.S;
+  using Sh = BwdShape<N>;
+  constexpr size_t smem = 2 * Sh::BUF * sizeof(float);
+  static_assert(Sh::BUF >= Sh::HW * 32 * 8, "room for the helpers' sums");
+  const long long blocks = tiles_of(q.f.D, q.f.G, Sh::CH) * q.f.B * q.f.S;
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
   auto k = bwd_kernel<T, N>;
   e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  k<<<(unsigned)blocks, kBW * 32, smem, st>>>(q);
+  k<<<(unsigned)blocks, Sh::NT, smem, st>>>(q);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   const long long rows = (long long)q.f.B * q.f.T * q.f.G, quads = rows * N / 2;
@@ -1113,7 +1305,7 @@ kla_status kla_ssm_fwd(const void* u, const void* dt, const float* A, const void
   a.B = B; a.T = T; a.D = D; a.G = G; a.S = sp.S; a.seg = sp.seg;
   a.softplus = softplus != 0;
   set_rows(a, ldu, lddt, ldb, ldc, ldz, N, es);
-  KLA_SSM_DISPATCH((e = run_forward<TY, KN, FULL>(a, st)))
+  KLA_SSM_DISPATCH((e = run_forward<TY, KN>(a, st)))
   return e == cudaSuccess ? KLA_OK : KLA_ERR_CUDA;
 }
 
