@@ -514,28 +514,42 @@ struct BwdArgs {
   float* part_d;                // [B*S][2][D]: dD, ddt_bias
 };
 
-// v[j], j < 4: lane nl ends with the sum over the LPC lanes of a channel of
-// token (nl & 3) (LPC >= 4: in v[0]) or of tokens nl, nl + 2 (LPC = 2).
+// v[q][j], j < 4 tokens of 6 quantities: lane nl ends with the sum over the LPC
+// lanes of a channel of token (nl & 3) (LPC >= 4: in v[q][0]) or of tokens nl,
+// nl + 2 (LPC = 2).  All quantities cross together, so that their exchanges
+// wait for each other once a round.
 template <int LPC>
-__device__ __forceinline__ void token_sums(float (&v)[4], int nl) {
+__device__ __forceinline__ void token_sums(float (&v)[6][4], int nl) {
   if constexpr (LPC == 2) {
 #pragma unroll
-    for (int j = 0; j < 4; j += 2) {  // tokens j, j + 1
-      const float keep = (nl & 1) ? v[j + 1] : v[j], send = (nl & 1) ? v[j] : v[j + 1];
-      v[j] = keep + __shfl_xor_sync(0xffffffffu, send, 1);
-    }
+    for (int q = 0; q < 6; ++q)
+#pragma unroll
+      for (int j = 0; j < 4; j += 2) {  // tokens j, j + 1
+        const float keep = (nl & 1) ? v[q][j + 1] : v[q][j];
+        const float send = (nl & 1) ? v[q][j] : v[q][j + 1];
+        v[q][j] = keep + __shfl_xor_sync(0xffffffffu, send, 1);
+      }
   } else {
 #pragma unroll
     for (int off = LPC / 2; off >= 4; off >>= 1)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) v[j] += __shfl_xor_sync(0xffffffffu, v[j], off);
-    const bool up = (nl & 2) != 0;
-    const float k0 = up ? v[2] : v[0], s0 = up ? v[0] : v[2];
-    const float k1 = up ? v[3] : v[1], s1 = up ? v[1] : v[3];
-    v[0] = k0 + __shfl_xor_sync(0xffffffffu, s0, 2);
-    v[1] = k1 + __shfl_xor_sync(0xffffffffu, s1, 2);
-    const float k = (nl & 1) ? v[1] : v[0], s = (nl & 1) ? v[0] : v[1];
-    v[0] = k + __shfl_xor_sync(0xffffffffu, s, 1);
+      for (int q = 0; q < 6; ++q)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[q][j] += __shfl_xor_sync(0xffffffffu, v[q][j], off);
+#pragma unroll
+    for (int off = 2; off > 0; off >>= 1) {
+      const bool up = (nl & off) != 0;
+      float got[6][2];
+#pragma unroll
+      for (int q = 0; q < 6; ++q)
+#pragma unroll
+        for (int j = 0; j < off; ++j)
+          got[q][j] = __shfl_xor_sync(0xffffffffu, up ? v[q][j] : v[q][j + off], off);
+#pragma unroll
+      for (int q = 0; q < 6; ++q)
+#pragma unroll
+        for (int j = 0; j < off; ++j) v[q][j] = (up ? v[q][j + off] : v[q][j]) + got[q][j];
+    }
   }
 }
 
@@ -777,28 +791,38 @@ bwd_kernel(BwdArgs q) {
     dA[c][0] = dA[c][1] = pack2(0.f, 0.f);
   }
   const int nck = (p.T + K - 1) / K;
+  struct {
+    float4 h[2], w[2];
+    float s[2];
+  } saved;
+  auto fetch = [&](int k) {
+    const int t = t_lo + k * K;
+    const long long ck = (long long)b * nck + t / K;
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      saved.h[c] = row(p.ckpt + ck * p.D * N, c);
+      if (q.fS > 1) {
+        saved.w[c] = row(q.fends + ((long long)b * q.fS + t / q.fseg) * p.D * N, c);
+        saved.s[c] = cc + c < nc ? p.cums[ck * p.D + c0 + cc + c] : 0.f;
+      }
+    }
+  };
+  fetch(ntile - 1);
   __syncthreads();
   for (int k = ntile - 1; k >= 0; --k) {
     float* buf = smem + (k & 1) * Sh::BUF;
     const float* sd = buf + cc;
     const float* sb = buf + 6 * Sh::XS + ord * N + nl * 4;
-    // the state before the tile's first token
+    // the state before the tile's first token, loaded during the tile before
     f32x2 h0[2][2];
-    {
-      const int t = t_lo + k * K;
-      const long long ck = (long long)b * nck + t / K;
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const float4 v = row(p.ckpt + ck * p.D * N, c);
-        h0[c][0] = pack2(v.x, v.y);
-        h0[c][1] = pack2(v.z, v.w);
-        if (q.fS > 1) {  // saved from a zero start: add what the segment's start left
-          const float4 w = row(q.fends + ((long long)b * q.fS + t / q.fseg) * p.D * N, c);
-          const float s = cc + c < nc ? p.cums[ck * p.D + c0 + cc + c] : 0.f;
-          const f32x2 s2 = pack2(s, s);
-          h0[c][0] = fma2(ex2_2(mul2(s2, a2[c][0])), pack2(w.x, w.y), h0[c][0]);
-          h0[c][1] = fma2(ex2_2(mul2(s2, a2[c][1])), pack2(w.z, w.w), h0[c][1]);
-        }
+    for (int c = 0; c < 2; ++c) {
+      h0[c][0] = pack2(saved.h[c].x, saved.h[c].y);
+      h0[c][1] = pack2(saved.h[c].z, saved.h[c].w);
+      if (q.fS > 1) {  // saved from a zero start: add what the segment's start left
+        const f32x2 s2 = pack2(saved.s[c], saved.s[c]);
+        h0[c][0] = fma2(ex2_2(mul2(s2, a2[c][0])), pack2(saved.w[c].x, saved.w[c].y), h0[c][0]);
+        h0[c][1] = fma2(ex2_2(mul2(s2, a2[c][1])), pack2(saved.w[c].z, saved.w[c].w), h0[c][1]);
       }
     }
     f32x2 tA[2][2];
@@ -828,7 +852,8 @@ bwd_kernel(BwdArgs q) {
         for (int c = 0; c < 2; ++c) { h[i + 1][c][0] = h[i][c][0]; h[i + 1][c][1] = h[i][c][1]; }
         forward(tb + i, h[i + 1], a[i]);
       }
-      float vB[2][4], vA[2][4], vY[2][4];
+      float v6[6][4];    // sum dh B, sum A h e, y0 of two channels
+      f32x2 bc[4][4];    // dB, dC of the thread's 4 states
 #pragma unroll
       for (int i = 3; i >= 0; --i) {
         const int t = tb + i;
@@ -849,58 +874,81 @@ bwd_kernel(BwdArgs q) {
           wC[0] = c ? fma2(h[i + 1][c][0], g2, wC[0]) : mul2(h[i + 1][c][0], g2);
           wC[1] = c ? fma2(h[i + 1][c][1], g2, wC[1]) : mul2(h[i + 1][c][1], g2);
           const float2 y = unpack2(fma2(cv.y, h[i + 1][c][1], mul2(cv.x, h[i + 1][c][0])));
-          vY[c][i] = y.x + y.y;
+          v6[4 + c][i] = y.x + y.y;
           const float2 sB = unpack2(fma2(dh1, bv.y, mul2(dh0, bv.x)));
-          vB[c][i] = sB.x + sB.y;
+          v6[c][i] = sB.x + sB.y;
           e[c][0] = mul2(a[i][c][0], dh0);
           e[c][1] = mul2(a[i][c][1], dh1);
           const f32x2 f0 = mul2(e[c][0], h[i][c][0]), f1 = mul2(e[c][1], h[i][c][1]);
           const float2 sA = unpack2(fma2(a2[c][1], f1, mul2(a2[c][0], f0)));
-          vA[c][i] = sA.x + sA.y;
+          v6[2 + c][i] = sA.x + sA.y;
           tA[c][0] = fma2(d2, f0, tA[c][0]);
           tA[c][1] = fma2(d2, f1, tA[c][1]);
         }
-        // dB, dC over the warp's channels
-        const float2 b01 = unpack2(wB[0]), b23 = unpack2(wB[1]), c01 = unpack2(wC[0]),
-                     c23 = unpack2(wC[1]);
-        float rb0 = b01.x + __shfl_xor_sync(0xffffffffu, b01.y, LPC);
-        float rb2 = b23.x + __shfl_xor_sync(0xffffffffu, b23.y, LPC);
-        float rc0 = c01.x + __shfl_xor_sync(0xffffffffu, c01.y, LPC);
-        float rc2 = c23.x + __shfl_xor_sync(0xffffffffu, c23.y, LPC);
-        float* o = buf + 6 * Sh::XS + 2 * Sh::BS + (warp * K + t) * 2 * N + nl * 4;
-        if constexpr (CL == 2) {
-          o[ord] = rb0;
-          o[2 ^ ord] = rb2;
-          o[N + ord] = rc0;
-          o[N + (2 ^ ord)] = rc2;
-        } else {
-          rb0 += __shfl_xor_sync(0xffffffffu, rb2, 2 * LPC);
-          rc0 += __shfl_xor_sync(0xffffffffu, rc2, 2 * LPC);
-          if constexpr (CL == 4) {
-            o[ord] = rb0;
-            o[N + ord] = rc0;
-          } else {
-            const bool up = (cg & 4) != 0;
-            float v = up ? rc0 : rb0;
-            v += __shfl_xor_sync(0xffffffffu, up ? rb0 : rc0, 4 * LPC);
-            if constexpr (CL == 16) v += __shfl_xor_sync(0xffffffffu, v, 8 * LPC);
-            if (CL == 8 || cg < 8) o[(up ? N : 0) + ord] = v;
+        bc[i][0] = wB[0]; bc[i][1] = wB[1];
+        bc[i][2] = wC[0]; bc[i][3] = wC[1];
+      }
+      // dB, dC over the warp's channels, the 4 tokens of a round together
+      float r[4][4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          r[i][j] = __shfl_xor_sync(0xffffffffu, unpack2(bc[i][j]).y, LPC);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) r[i][j] += unpack2(bc[i][j]).x;
+      float* o = buf + 6 * Sh::XS + 2 * Sh::BS + (warp * K + tb) * 2 * N + nl * 4;
+      if constexpr (CL == 2) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          o[i * 2 * N + ord] = r[i][0];
+          o[i * 2 * N + (2 ^ ord)] = r[i][1];
+          o[i * 2 * N + N + ord] = r[i][2];
+          o[i * 2 * N + N + (2 ^ ord)] = r[i][3];
+        }
+      } else {
+        float x[4][2];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+            x[i][j] = __shfl_xor_sync(0xffffffffu, r[i][2 * j + 1], 2 * LPC);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) x[i][j] += r[i][2 * j];
+        if constexpr (CL == 4) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            o[i * 2 * N + ord] = x[i][0];
+            o[i * 2 * N + N + ord] = x[i][1];
           }
+        } else {
+          const bool up = (cg & 4) != 0;
+          float w[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            w[i] = __shfl_xor_sync(0xffffffffu, up ? x[i][0] : x[i][1], 4 * LPC);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) w[i] += up ? x[i][1] : x[i][0];
+          if constexpr (CL == 16)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[i] += __shfl_xor_sync(0xffffffffu, w[i], 8 * LPC);
+          if (CL == 8 || cg < 8)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[i * 2 * N + (up ? N : 0) + ord] = w[i];
         }
       }
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        token_sums<LPC>(vB[c], nl);
-        token_sums<LPC>(vA[c], nl);
-        token_sums<LPC>(vY[c], nl);
-      }
+      token_sums<LPC>(v6, nl);
       if (LPC <= 4 || nl < 4) {
 #pragma unroll
         for (int j = 0; j < (LPC == 2 ? 4 : 1); j += 2) {
           float* o = buf + 3 * Sh::XS + (tb + j + nl) * CH + cc;
-          *reinterpret_cast<float2*>(o) = make_float2(vB[0][j], vB[1][j]);
-          *reinterpret_cast<float2*>(o + Sh::XS) = make_float2(vA[0][j], vA[1][j]);
-          *reinterpret_cast<float2*>(o + 2 * Sh::XS) = make_float2(vY[0][j], vY[1][j]);
+          *reinterpret_cast<float2*>(o) = make_float2(v6[0][j], v6[1][j]);
+          *reinterpret_cast<float2*>(o + Sh::XS) = make_float2(v6[2][j], v6[3][j]);
+          *reinterpret_cast<float2*>(o + 2 * Sh::XS) = make_float2(v6[4][j], v6[5][j]);
         }
       }
     };
@@ -910,6 +958,7 @@ bwd_kernel(BwdArgs q) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) forward(i, hm, skip_a);
     half(4, hm);
+    if (k > 0) fetch(k - 1);
     half(0, h0);
 #pragma unroll
     for (int c = 0; c < 2; ++c) {  // per tile first: shorter chains of additions
