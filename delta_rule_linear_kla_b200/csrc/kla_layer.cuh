@@ -196,6 +196,27 @@ __device__ __forceinline__ Raw4<T> ld_raw4(const T* p, int n, bool vec) {
   return v;
 }
 
+// Copies of 16 or 4 bytes to shared memory that hold no register while they are
+// in flight; cp_wait waits for all but the last KEEP committed groups of this
+// thread.
+__device__ __forceinline__ void cp16(void* to, const void* from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                   (uint32_t)__cvta_generic_to_shared(to)),
+               "l"(from)
+               : "memory");
+}
+__device__ __forceinline__ void cp4(void* to, const void* from) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(
+                   (uint32_t)__cvta_generic_to_shared(to)),
+               "l"(from)
+               : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int KEEP>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(KEEP) : "memory");
+}
+
 // Tokens of sequence b that exist: lengths[b] clamped to [0, T] (no lengths:
 // all T).
 __device__ __forceinline__ int live_tokens(const int* lengths, int b, int T) {

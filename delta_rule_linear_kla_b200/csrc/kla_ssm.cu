@@ -791,21 +791,34 @@ bwd_kernel(BwdArgs q) {
     dA[c][0] = dA[c][1] = pack2(0.f, 0.f);
   }
   const int nck = (p.T + K - 1) / K;
-  struct {
-    float4 h[2], w[2];
-    float s[2];
-  } saved;
+  // a tile's saved states come to places of this thread's own, one tile ahead:
+  // [2][4][CW * 32] rows (state and segment start of both channels), [2][CW * 32]
+  // sums of dt'
+  float4* const s_h = reinterpret_cast<float4*>(smem + 2 * Sh::BUF) + tid;
+  float2* const s_s = reinterpret_cast<float2*>(s_h - tid + 8 * CW * 32) + tid;
+  if (cc + 1 >= nc) {  // channels that do not exist are never copied
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s_h[i * CW * 32] = make_float4(0.f, 0.f, 0.f, 0.f);
+    s_s[0] = s_s[CW * 32] = make_float2(0.f, 0.f);
+  }
   auto fetch = [&](int k) {
     const int t = t_lo + k * K;
     const long long ck = (long long)b * nck + t / K;
+    float4* v = s_h + (k & 1) * 4 * CW * 32;
+    float* sum = reinterpret_cast<float*>(s_s + (k & 1) * CW * 32);
+    const long long at = (long long)(c0 + cc) * N + nl * 4;
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
-      saved.h[c] = row(p.ckpt + ck * p.D * N, c);
-      if (q.fS > 1) {
-        saved.w[c] = row(q.fends + ((long long)b * q.fS + t / q.fseg) * p.D * N, c);
-        saved.s[c] = cc + c < nc ? p.cums[ck * p.D + c0 + cc + c] : 0.f;
+      if (cc + c < nc) {
+        cp16(v + c * CW * 32, p.ckpt + ck * p.D * N + at + c * N);
+        if (q.fS > 1) {
+          cp16(v + (2 + c) * CW * 32,
+               q.fends + ((long long)b * q.fS + t / q.fseg) * p.D * N + at + c * N);
+          cp4(sum + c, p.cums + ck * p.D + c0 + cc + c);
+        }
       }
     }
+    cp_commit();
   };
   fetch(ntile - 1);
   __syncthreads();
@@ -813,16 +826,28 @@ bwd_kernel(BwdArgs q) {
     float* buf = smem + (k & 1) * Sh::BUF;
     const float* sd = buf + cc;
     const float* sb = buf + 6 * Sh::XS + ord * N + nl * 4;
-    // the state before the tile's first token, loaded during the tile before
+    // the state before the tile's first token
     f32x2 h0[2][2];
+    if (k > 0) {
+      fetch(k - 1);
+      cp_wait<1>();
+    } else {
+      cp_wait<0>();
+    }
+    {
+      const float4* v = s_h + (k & 1) * 4 * CW * 32;
+      const float2 s = s_s[(k & 1) * CW * 32];
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      h0[c][0] = pack2(saved.h[c].x, saved.h[c].y);
-      h0[c][1] = pack2(saved.h[c].z, saved.h[c].w);
-      if (q.fS > 1) {  // saved from a zero start: add what the segment's start left
-        const f32x2 s2 = pack2(saved.s[c], saved.s[c]);
-        h0[c][0] = fma2(ex2_2(mul2(s2, a2[c][0])), pack2(saved.w[c].x, saved.w[c].y), h0[c][0]);
-        h0[c][1] = fma2(ex2_2(mul2(s2, a2[c][1])), pack2(saved.w[c].z, saved.w[c].w), h0[c][1]);
+      for (int c = 0; c < 2; ++c) {
+        const float4 h = reorder(v[c * CW * 32], ord);
+        h0[c][0] = pack2(h.x, h.y);
+        h0[c][1] = pack2(h.z, h.w);
+        if (q.fS > 1) {  // saved from a zero start: add what the segment's start left
+          const float4 w = reorder(v[(2 + c) * CW * 32], ord);
+          const f32x2 s2 = c ? pack2(s.y, s.y) : pack2(s.x, s.x);
+          h0[c][0] = fma2(ex2_2(mul2(s2, a2[c][0])), pack2(w.x, w.y), h0[c][0]);
+          h0[c][1] = fma2(ex2_2(mul2(s2, a2[c][1])), pack2(w.z, w.w), h0[c][1]);
+        }
       }
     }
     f32x2 tA[2][2];
@@ -958,7 +983,6 @@ bwd_kernel(BwdArgs q) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) forward(i, hm, skip_a);
     half(4, hm);
-    if (k > 0) fetch(k - 1);
     half(0, h0);
 #pragma unroll
     for (int c = 0; c < 2; ++c) {  // per tile first: shorter chains of additions
@@ -1091,30 +1115,42 @@ struct Split {
   int S, seg;
 };
 
-// Segments: none while the channel tiles alone give every SM a block.  A cut
-// runs the exponentials twice, so it has to bring at least that: as many
-// segments as fill two blocks an SM, of 256 tokens at least.
-static Split split(long long base, int T) {
+// Segments of a sequence.  `tiles` blocks would run uncut; a block's time a
+// token is, in units of a scan block that shares an SM, 1.2 alone and n on an
+// SM with n of them (8 x 4096 x 2048 x 16, two an SM: 220 clocks a token; one:
+// 130).  A cut scan first needs all segments but one for their end states
+// (about 0.8 of a scan each), so the parts have to bring more than that: the
+// fewest segments of at least 128 tokens whose modelled time is within 3 % of
+// the best.
+//   ends: what a segment's end state costs beside `own`, its time in the pass
+//   itself (1 for the scan; 3.5 for the backward pass: 780 clocks, two an SM)
+static Split split(long long tiles, int T, double own, double ends) {
+  auto block = [](long long n) { return n <= 148 ? 1.2 : (double)((n + 147) / 148); };
+  auto time = [&](int S) {
+    return (own * block(tiles * S) + (S > 1 ? ends * block(tiles * (S - 1)) : 0.0)) / S;
+  };
+  const int most = T / 128 < 64 ? T / 128 : 64;
+  double best = time(1);
+  for (int S = 2; S <= most; ++S) best = time(S) < best ? time(S) : best;
   int S = 1;
-  if (base < 148) {
-    const long long want = (2 * 148) / base;
-    const int most = T / 256;
-    S = (int)(want < most ? want : most);
-    if (S < 3) S = 1;
-  }
-  const int tiles = (T + kTile - 1) / kTile;
-  const int seg = ((tiles + S - 1) / S) * kTile;
-  S = (T + seg - 1) / seg;
-  return Split{S < 1 ? 1 : S, seg < kTile ? kTile : seg};
+  while (S < most && time(S) > 1.03 * best) ++S;
+  const int blocks = (T + kTile - 1) / kTile;
+  const int seg = ((blocks + S - 1) / S) * kTile;
+  return Split{(T + seg - 1) / seg, seg};
 }
 
 static long long tiles_of(int D, int G, int CH) { return (long long)G * ((D / G + CH - 1) / CH); }
 
 static Split fwd_split(int B, int T, int D, int G, int N) {
-  return split(B * tiles_of(D, G, channels(N)), T);
+  return split(B * tiles_of(D, G, channels(N)), T, 1.0, 0.8);
+}
+// the saved states need no second pass: the backward kernel adds what a
+// segment's start leaves
+static Split save_split(int B, int T, int D, int G, int N) {
+  return split(B * tiles_of(D, G, channels(N)), T, 0.8, 0.0);
 }
 static Split bwd_split(int B, int T, int D, int G, int N) {
-  return split(B * tiles_of(D, G, bwd_channels(N)), T);
+  return split(B * tiles_of(D, G, bwd_channels(N)), T, 3.5, 0.8);
 }
 
 static size_t up(size_t x) { return (x + 255) & ~(size_t)255; }
@@ -1163,7 +1199,7 @@ struct BwdPlan {
 
 static BwdPlan bwd_plan(int B, int T, int D, int G, int N) {
   BwdPlan w;
-  w.f = fwd_split(B, T, D, G, N);
+  w.f = save_split(B, T, D, G, N);
   w.r = bwd_split(B, T, D, G, N);
   w.TPG = (D / G + bwd_channels(N) - 1) / bwd_channels(N);
   const size_t dn = (size_t)D * N * 4, nck = (size_t)B * ((T + kCkpt - 1) / kCkpt);
@@ -1208,7 +1244,8 @@ static cudaError_t run_backward(BwdArgs q, const BwdPlan& w, unsigned char* ws, 
     if (e != cudaSuccess) return e;
   }
   using Sh = BwdShape<N>;
-  constexpr size_t smem = 2 * Sh::BUF * sizeof(float);
+  // two buffers, and two tiles' saved states of every recurrence thread
+  constexpr size_t smem = 2 * (Sh::BUF * sizeof(float) + Sh::CW * 32 * (4 * 16 + 8));
   static_assert(Sh::BUF >= Sh::HW * 32 * 8, "room for the helpers' sums");
   const long long blocks = tiles_of(q.f.D, q.f.G, Sh::CH) * q.f.B * q.f.S;
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
