@@ -7,6 +7,8 @@
 // with x[-W+1 .. -1] the state s0 (the last W-1 inputs of what came before).
 // All arithmetic is fp32; only y (and dx, ds0) are rounded, once, to the
 // activations' type.
+#include <type_traits>
+
 #include "kla_layer.cuh"
 
 namespace kla {
@@ -14,82 +16,53 @@ namespace conv {
 
 using namespace layer;
 
-// Eight (bf16) or four (fp32) channels at a time where rows allow 16-byte
-// accesses, one channel otherwise.
+// V channels of one row as they lie in memory, and as P packed pairs of fp32
+// (a single channel leaves the second of its pair 0).
+template <int V>
+constexpr int kPairs = (V + 1) / 2;
+
 template <typename T, int V>
-struct Row;
-template <>
-struct Row<__nv_bfloat16, 8> {
-  uint4 r;
-  __device__ __forceinline__ void load(const __nv_bfloat16* p) {
-    r = *reinterpret_cast<const uint4*>(p);
-  }
-  __device__ __forceinline__ void zero() { r = make_uint4(0, 0, 0, 0); }
-  __device__ __forceinline__ void get(float (&f)[8]) const {
-    const uint32_t u[4] = {r.x, r.y, r.z, r.w};
+struct Row {
+  static constexpr int P = kPairs<V>;
+  static constexpr int B = sizeof(T) * V;  // 2 .. 16 bytes
+  using Raw = typename std::conditional<
+      B == 16, uint4, typename std::conditional<B == 8, uint2, T>::type>::type;
+  Raw r;
+  __device__ __forceinline__ void load(const T* p) { r = *reinterpret_cast<const Raw*>(p); }
+  __device__ __forceinline__ void store(T* p) const { *reinterpret_cast<Raw*>(p) = r; }
+  __device__ __forceinline__ void zero() { r = Raw{}; }
+  __device__ __forceinline__ void get(f32x2 (&f)[P]) const {
+    if constexpr (V == 1) {
+      f[0] = pack2(IO<T>::ld(reinterpret_cast<const T*>(&r)), 0.f);
+    } else {
+      const uint32_t* u = reinterpret_cast<const uint32_t*>(&r);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      f[2 * i] = __uint_as_float(u[i] << 16);
-      f[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+      for (int i = 0; i < P; ++i) {
+        if constexpr (sizeof(T) == 2)
+          f[i] = pack2(__uint_as_float(u[i] << 16), __uint_as_float(u[i] & 0xffff0000u));
+        else
+          f[i] = pack2(__uint_as_float(u[2 * i]), __uint_as_float(u[2 * i + 1]));
+      }
     }
   }
-  __device__ __forceinline__ void set(const float (&f)[8]) {
-    uint32_t u[4];
+  __device__ __forceinline__ void set(const f32x2 (&f)[P]) {
+    if constexpr (V == 1) {
+      IO<T>::st(reinterpret_cast<T*>(&r), unpack2(f[0]).x);
+    } else {
+      uint32_t* u = reinterpret_cast<uint32_t*>(&r);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
-      u[i] = *reinterpret_cast<uint32_t*>(&h);
+      for (int i = 0; i < P; ++i) {
+        const float2 v = unpack2(f[i]);
+        if constexpr (sizeof(T) == 2) {
+          __nv_bfloat162 h = __floats2bfloat162_rn(v.x, v.y);
+          u[i] = *reinterpret_cast<uint32_t*>(&h);
+        } else {
+          u[2 * i] = __float_as_uint(v.x);
+          u[2 * i + 1] = __float_as_uint(v.y);
+        }
+      }
     }
-    r = make_uint4(u[0], u[1], u[2], u[3]);
   }
-  __device__ __forceinline__ void store(__nv_bfloat16* p) const {
-    *reinterpret_cast<uint4*>(p) = r;
-  }
-};
-template <>
-struct Row<__nv_bfloat16, 4> {
-  uint2 r;
-  __device__ __forceinline__ void load(const __nv_bfloat16* p) {
-    r = *reinterpret_cast<const uint2*>(p);
-  }
-  __device__ __forceinline__ void zero() { r = make_uint2(0, 0); }
-  __device__ __forceinline__ void get(float (&f)[4]) const {
-    f[0] = __uint_as_float(r.x << 16);
-    f[1] = __uint_as_float(r.x & 0xffff0000u);
-    f[2] = __uint_as_float(r.y << 16);
-    f[3] = __uint_as_float(r.y & 0xffff0000u);
-  }
-  __device__ __forceinline__ void set(const float (&f)[4]) {
-    __nv_bfloat162 a = __floats2bfloat162_rn(f[0], f[1]), b = __floats2bfloat162_rn(f[2], f[3]);
-    r = make_uint2(*reinterpret_cast<uint32_t*>(&a), *reinterpret_cast<uint32_t*>(&b));
-  }
-  __device__ __forceinline__ void store(__nv_bfloat16* p) const {
-    *reinterpret_cast<uint2*>(p) = r;
-  }
-};
-template <>
-struct Row<float, 4> {
-  float4 r;
-  __device__ __forceinline__ void load(const float* p) {
-    r = *reinterpret_cast<const float4*>(p);
-  }
-  __device__ __forceinline__ void zero() { r = make_float4(0.f, 0.f, 0.f, 0.f); }
-  __device__ __forceinline__ void get(float (&f)[4]) const {
-    f[0] = r.x; f[1] = r.y; f[2] = r.z; f[3] = r.w;
-  }
-  __device__ __forceinline__ void set(const float (&f)[4]) {
-    r = make_float4(f[0], f[1], f[2], f[3]);
-  }
-  __device__ __forceinline__ void store(float* p) const { *reinterpret_cast<float4*>(p) = r; }
-};
-template <typename T>
-struct Row<T, 1> {
-  T r;
-  __device__ __forceinline__ void load(const T* p) { r = *p; }
-  __device__ __forceinline__ void zero() { IO<T>::st(&r, 0.f); }
-  __device__ __forceinline__ void get(float (&f)[1]) const { f[0] = IO<T>::ld(&r); }
-  __device__ __forceinline__ void set(const float (&f)[1]) { IO<T>::st(&r, f[0]); }
-  __device__ __forceinline__ void store(T* p) const { *p = r; }
 };
 
 // Row i of a sequence's inputs, i in [-(W-1), T): the state before 0.
@@ -106,14 +79,59 @@ __device__ __forceinline__ Row<T, V> input_row(const T* xb, long long ldx, const
   return r;
 }
 
+// The W taps and the bias of V channels from c, as pairs; a channel's taps are
+// one 16- or 8-byte access for W = 4 or 2.
 template <int V, int W>
 __device__ __forceinline__ void load_taps(const float* w, const float* bias, int c,
-                                          float (&tap)[W][V], float (&b0)[V]) {
+                                          f32x2 (&tap)[W][kPairs<V>], f32x2 (&b0)[kPairs<V>]) {
+  float f[2][W], q[2];
 #pragma unroll
-  for (int e = 0; e < V; ++e) {
+  for (int i = 0; i < kPairs<V>; ++i) {
 #pragma unroll
-    for (int j = 0; j < W; ++j) tap[j][e] = w[(long long)(c + e) * W + j];
-    b0[e] = bias ? bias[c + e] : 0.f;
+    for (int k = 0; k < 2; ++k) {
+      const bool in = 2 * i + k < V;
+      const float* p = w + (long long)(c + 2 * i + k) * W;
+      if constexpr (W == 4) {
+        const float4 v = in ? *reinterpret_cast<const float4*>(p) : make_float4(0, 0, 0, 0);
+        f[k][0] = v.x; f[k][1] = v.y; f[k][2] = v.z; f[k][3] = v.w;
+      } else if constexpr (W == 2) {
+        const float2 v = in ? *reinterpret_cast<const float2*>(p) : make_float2(0, 0);
+        f[k][0] = v.x; f[k][1] = v.y;
+      } else {
+#pragma unroll
+        for (int j = 0; j < W; ++j) f[k][j] = in ? p[j] : 0.f;
+      }
+      q[k] = in && bias ? bias[c + 2 * i + k] : 0.f;
+    }
+#pragma unroll
+    for (int j = 0; j < W; ++j) tap[j][i] = pack2(f[0][j], f[1][j]);
+    b0[i] = pack2(q[0], q[1]);
+  }
+}
+
+// p = bias + sum of the taps, oldest first
+template <int V, int W>
+__device__ __forceinline__ void taps_sum(const f32x2 (&tap)[W][kPairs<V>],
+                                         const f32x2 (&b0)[kPairs<V>],
+                                         const f32x2 (&win)[W - 1][kPairs<V>],
+                                         const f32x2 (&cur)[kPairs<V>], f32x2 (&p)[kPairs<V>]) {
+#pragma unroll
+  for (int i = 0; i < kPairs<V>; ++i) {
+    p[i] = b0[i];
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j) p[i] = fma2(tap[j][i], win[j][i], p[i]);
+    p[i] = fma2(tap[W - 1][i], cur[i], p[i]);
+  }
+}
+
+template <int V, int W>
+__device__ __forceinline__ void shift(f32x2 (&win)[W - 1][kPairs<V>],
+                                      const f32x2 (&cur)[kPairs<V>]) {
+#pragma unroll
+  for (int i = 0; i < kPairs<V>; ++i) {
+#pragma unroll
+    for (int j = 0; j + 1 < W - 1; ++j) win[j][i] = win[j + 1][i];
+    win[W - 2][i] = cur[i];
   }
 }
 
@@ -122,14 +140,20 @@ __device__ __forceinline__ void load_taps(const float* w, const float* bias, int
 // Bound by HBM: one read of x and one write of y.  A thread walks L tokens of
 // V channels with the last W-1 inputs in registers, so that x is read once
 // but for W-1 rows at the start of each walk (from L2); neighbouring lanes
-// hold neighbouring channels.  Four rows are loaded before the first is used.
+// hold neighbouring channels.  Four rows are in flight while the four before
+// are computed, on packed pairs of channels.  Blocks of 128 threads at 72
+// registers, 28 warps an SM, carry enough loads: 8 x 4096 x 2048 bf16 takes
+// 57 us, 4.7 TB/s (64 us with 256 threads at 64 registers, 107 us with eight
+// channels a thread).
+constexpr int kFT = 128;
 template <typename T, int V, int W, bool SILU>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(kFT, 7)
 conv_fwd_kernel(const T* __restrict__ x, long long ldx, const float* __restrict__ w,
                 const float* __restrict__ bias, const T* __restrict__ s0,
                 const int* __restrict__ lengths, T* __restrict__ y, T* __restrict__ sT,
                 int Tn, int D, int CG, int NB, int L, long long total) {
-  const long long id = (long long)blockIdx.x * 256 + threadIdx.x;
+  constexpr int P = kPairs<V>;
+  const long long id = (long long)blockIdx.x * kFT + threadIdx.x;
   if (id >= total) return;
   const int cg = (int)(id % CG);
   const long long rest = id / CG;
@@ -140,46 +164,57 @@ conv_fwd_kernel(const T* __restrict__ x, long long ldx, const float* __restrict_
   const T* s0b = s0 ? s0 + (long long)b * (W - 1) * D + c : nullptr;
   T* yb = y + (long long)b * Tn * D + c;
 
-  float tap[W][V], b0[V];
-  load_taps<V, W>(w, bias, c, tap, b0);
-
   const int t0 = tb * L, t1 = min(Tn, t0 + L), tn = min(t1, n);
-  float win[W - 1][V];  // win[j] = row t - (W-1) + j
+  Row<T, V> next[4];
+  auto fetch = [&](int t) {
+    const T* px = xb + (long long)t * ldx;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      next[i].load(px);
+      px += ldx;
+    }
+  };
+  if (t0 + 4 <= tn) fetch(t0);
+  f32x2 tap[W][P], b0[P], win[W - 1][P];  // win[j] = row t - (W-1) + j
+  load_taps<V, W>(w, bias, c, tap, b0);
   if (t0 < tn) {
 #pragma unroll
     for (int j = 0; j < W - 1; ++j)
       input_row<T, V, W>(xb, ldx, s0b, D, t0 - (W - 1) + j).get(win[j]);
   }
-  auto one = [&](const Row<T, V>& r, int t) {
-    float cur[V], out[V];
+  auto one = [&](const Row<T, V>& r, T* to) {
+    f32x2 cur[P], p[P];
     r.get(cur);
+    taps_sum<V, W>(tap, b0, win, cur, p);
+    shift<V, W>(win, cur);
+    if (SILU)
 #pragma unroll
-    for (int e = 0; e < V; ++e) {
-      float p = b0[e];
-#pragma unroll
-      for (int j = 0; j < W - 1; ++j) p = fmaf(tap[j][e], win[j][e], p);
-      p = fmaf(tap[W - 1][e], cur[e], p);
-      out[e] = SILU ? silu(p) : p;
-#pragma unroll
-      for (int j = 0; j + 1 < W - 1; ++j) win[j][e] = win[j + 1][e];
-      win[W - 2][e] = cur[e];
-    }
+      for (int i = 0; i < P; ++i) {
+        const float2 v = unpack2(p[i]);
+        p[i] = pack2(silu(v.x), silu(v.y));
+      }
     Row<T, V> o;
-    o.set(out);
-    o.store(yb + (long long)t * D);
+    o.set(p);
+    o.store(to);
   };
   int t = t0;
-  for (; t + 4 <= tn; t += 4) {
+  T* py = yb + (long long)t * D;
+  while (t + 4 <= tn) {
     Row<T, V> r[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) r[i].load(xb + (long long)(t + i) * ldx);
+    for (int i = 0; i < 4; ++i) r[i] = next[i];
+    t += 4;
+    if (t + 4 <= tn) fetch(t);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) one(r[i], t + i);
+    for (int i = 0; i < 4; ++i) {
+      one(r[i], py);
+      py += D;
+    }
   }
   for (; t < tn; ++t) {
     Row<T, V> r;
     r.load(xb + (long long)t * ldx);
-    one(r, t);
+    one(r, yb + (long long)t * D);
   }
   Row<T, V> zero;
   zero.zero();
@@ -212,13 +247,20 @@ conv_bwd_kernel(const T* __restrict__ x, long long ldx, const float* __restrict_
                 const int* __restrict__ lengths, const T* __restrict__ gy,
                 const T* __restrict__ gs, T* __restrict__ dx, T* __restrict__ ds0,
                 float* __restrict__ part, int Tn, int D, int CB, int NB, int L) {
+  constexpr int P = kPairs<V>;
   const int cb = blockIdx.x % CB;
   const int rest = blockIdx.x / CB;
   const int nb = rest % NB, b = rest / NB;  // this block's kBY * L tokens
   const int c = (cb * kBX + threadIdx.x) * V;
-  const bool live = c < D;
-  float dw[W][V] = {}, db[V] = {};
-  if (live) {
+  f32x2 dw[W][P], db[P];
+#pragma unroll
+  for (int i = 0; i < P; ++i) {
+    db[i] = pack2(0.f, 0.f);
+#pragma unroll
+    for (int j = 0; j < W; ++j) dw[j][i] = db[i];
+  }
+  const int t0 = (nb * kBY + threadIdx.y) * L;
+  if (c < D && t0 < Tn) {
     const int n = live_tokens(lengths, b, Tn);
     const T* xb = x + (long long)b * Tn * ldx + c;
     const T* s0b = s0 ? s0 + (long long)b * (W - 1) * D + c : nullptr;
@@ -226,86 +268,119 @@ conv_bwd_kernel(const T* __restrict__ x, long long ldx, const float* __restrict_
     const T* gsb = gs ? gs + (long long)b * (W - 1) * D + c : nullptr;
     T* db_x = dx + (long long)b * Tn * D + c;
     T* db_s = ds0 ? ds0 + (long long)b * (W - 1) * D + c : nullptr;
-    float tap[W][V], b0[V];
+    const int t1 = min(Tn, t0 + L), tn = min(t1, n);
+    Row<T, V> nx[4], ng[4];
+    auto fetch = [&](int t) {
+      const T *px = xb + (long long)t * ldx, *pg = gb + (long long)t * D;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        nx[i].load(px);
+        ng[i].load(pg);
+        px += ldx;
+        pg += D;
+      }
+    };
+    if (t0 + 4 <= tn) fetch(t0);
+    f32x2 tap[W][P], b0[P];
     load_taps<V, W>(w, bias, c, tap, b0);
-    const int t0 = (nb * kBY + threadIdx.y) * L;
-    const int t1 = min(Tn, t0 + L);
-    if (t0 < Tn) {
-      float win[W - 1][V];     // rows t - (W-1) .. t - 1
-      float dpw[W][V] = {};    // dpw[j] = dp[t - j]
+    f32x2 win[W - 1][P];  // rows t - (W-1) .. t - 1
+    f32x2 dpw[W - 1][P];  // dp[t - (W-1)] .. dp[t - 1]
 #pragma unroll
-      for (int j = 0; j < W - 1; ++j) {
-        if (t0 - (W - 1) + j < n)  // rows at or past the length are not read
-          input_row<T, V, W>(xb, ldx, s0b, D, t0 - (W - 1) + j).get(win[j]);
-        else
+    for (int j = 0; j < W - 1; ++j) {
+      Row<T, V> r;
+      r.zero();  // rows at or past the length are not read
+      if (t0 - (W - 1) + j < n) r = input_row<T, V, W>(xb, ldx, s0b, D, t0 - (W - 1) + j);
+      r.get(win[j]);
 #pragma unroll
-          for (int e = 0; e < V; ++e) win[j][e] = 0.f;
-      }
-      const int emit0 = t0 == 0 ? -(W - 1) : t0;
-#pragma unroll 4
-      for (int t = t0; t < t1 + W - 1; ++t) {
+      for (int i = 0; i < P; ++i) dpw[j][i] = pack2(0.f, 0.f);
+    }
+    // dp of token t, whose sums go to dw where it is one of the walk's own
+    auto grad = [&](const Row<T, V>& rx, const Row<T, V>& rg, bool own, f32x2 (&dp)[P]) {
+      f32x2 cur[P];
+      rx.get(cur);
+      rg.get(dp);
+      if (SILU) {
+        f32x2 p[P];
+        taps_sum<V, W>(tap, b0, win, cur, p);
 #pragma unroll
-        for (int j = W - 1; j > 0; --j)
-#pragma unroll
-          for (int e = 0; e < V; ++e) dpw[j][e] = dpw[j - 1][e];
-        if (t < n) {
-          Row<T, V> rx, rg;
-          rx.load(xb + (long long)t * ldx);
-          rg.load(gb + (long long)t * D);
-          float cur[V], g[V];
-          rx.get(cur);
-          rg.get(g);
-#pragma unroll
-          for (int e = 0; e < V; ++e) {
-            if (SILU) {
-              float p = b0[e];
-#pragma unroll
-              for (int j = 0; j < W - 1; ++j) p = fmaf(tap[j][e], win[j][e], p);
-              p = fmaf(tap[W - 1][e], cur[e], p);
-              const float s = sigmoid(p);
-              g[e] *= s * fmaf(p, 1.f - s, 1.f);
-            }
-            dpw[0][e] = g[e];
-            if (t < t1) {
-#pragma unroll
-              for (int j = 0; j < W - 1; ++j) dw[j][e] = fmaf(g[e], win[j][e], dw[j][e]);
-              dw[W - 1][e] = fmaf(g[e], cur[e], dw[W - 1][e]);
-              db[e] += g[e];
-            }
-#pragma unroll
-            for (int j = 0; j + 1 < W - 1; ++j) win[j][e] = win[j + 1][e];
-            win[W - 2][e] = cur[e];
-          }
-        } else {
-#pragma unroll
-          for (int e = 0; e < V; ++e) dpw[0][e] = 0.f;
-        }
-        const int i = t - (W - 1);
-        if (i >= emit0 && i < t1) {
-          float o[V];
-#pragma unroll
-          for (int e = 0; e < V; ++e) {
-            o[e] = 0.f;
-#pragma unroll
-            for (int j = 0; j < W; ++j) o[e] = fmaf(tap[j][e], dpw[j][e], o[e]);
-          }
-          const int r = i + (W - 1) - n;  // row of the final state that holds input i
-          if (gsb && r >= 0 && r < W - 1) {
-            Row<T, V> rs;
-            float f[V];
-            rs.load(gsb + (long long)r * D);
-            rs.get(f);
-#pragma unroll
-            for (int e = 0; e < V; ++e) o[e] += f[e];
-          }
-          Row<T, V> ro;
-          ro.set(o);
-          if (i >= 0)
-            ro.store(db_x + (long long)i * D);
-          else if (db_s)
-            ro.store(db_s + (long long)(W - 1 + i) * D);
+        for (int i = 0; i < P; ++i) {
+          const float2 v = unpack2(p[i]);
+          const f32x2 s = pack2(sigmoid(v.x), sigmoid(v.y)), one = pack2(1.f, 1.f);
+          dp[i] = mul2(dp[i], mul2(s, fma2(p[i], sub2(one, s), one)));
         }
       }
+      if (own) {
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+#pragma unroll
+          for (int j = 0; j < W - 1; ++j) dw[j][i] = fma2(dp[i], win[j][i], dw[j][i]);
+          dw[W - 1][i] = fma2(dp[i], cur[i], dw[W - 1][i]);
+          db[i] = add2(db[i], dp[i]);
+        }
+      }
+      shift<V, W>(win, cur);
+    };
+    // dx[t - (W-1)]
+    auto back = [&](const f32x2 (&dp)[P], f32x2 (&o)[P]) {
+#pragma unroll
+      for (int i = 0; i < P; ++i) {
+        o[i] = mul2(tap[0][i], dp[i]);
+#pragma unroll
+        for (int j = 1; j < W; ++j) o[i] = fma2(tap[j][i], dpw[W - 1 - j][i], o[i]);
+      }
+      shift<V, W>(dpw, dp);
+    };
+    int t = t0;
+    while (t + 4 <= tn) {
+      Row<T, V> rx[4], rg[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) { rx[i] = nx[i]; rg[i] = ng[i]; }
+      if (t + 8 <= tn) fetch(t + 4);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        f32x2 dp[P], o[P];
+        grad(rx[i], rg[i], true, dp);
+        back(dp, o);
+        const int at = t + i - (W - 1);
+        Row<T, V> ro;
+        ro.set(o);
+        if (at >= t0)
+          ro.store(db_x + (long long)at * D);
+        else if (t0 == 0 && db_s)
+          ro.store(db_s + (long long)(W - 1 + at) * D);
+      }
+      t += 4;
+    }
+    const int emit0 = t0 == 0 ? -(W - 1) : t0;
+    for (; t < t1 + W - 1; ++t) {
+      f32x2 dp[P], o[P];
+      if (t < n) {
+        Row<T, V> rx, rg;
+        rx.load(xb + (long long)t * ldx);
+        rg.load(gb + (long long)t * D);
+        grad(rx, rg, t < t1, dp);
+      } else {
+#pragma unroll
+        for (int i = 0; i < P; ++i) dp[i] = pack2(0.f, 0.f);
+      }
+      back(dp, o);
+      const int at = t - (W - 1);
+      if (at < emit0 || at >= t1) continue;
+      const int r = t - n;  // row of the final state that holds input `at`
+      if (gsb && r >= 0 && r < W - 1) {
+        Row<T, V> rs;
+        f32x2 f[P];
+        rs.load(gsb + (long long)r * D);
+        rs.get(f);
+#pragma unroll
+        for (int i = 0; i < P; ++i) o[i] = add2(o[i], f[i]);
+      }
+      Row<T, V> ro;
+      ro.set(o);
+      if (at >= 0)
+        ro.store(db_x + (long long)at * D);
+      else if (db_s)
+        ro.store(db_s + (long long)(W - 1 + at) * D);
     }
   }
   // block sums: [W + 1][kBX * V], one walk after the other
@@ -313,8 +388,12 @@ conv_bwd_kernel(const T* __restrict__ x, long long ldx, const float* __restrict_
 #pragma unroll
   for (int e = 0; e < V; ++e) {
 #pragma unroll
-    for (int j = 0; j < W; ++j) red[threadIdx.y][j][threadIdx.x * V + e] = dw[j][e];
-    red[threadIdx.y][W][threadIdx.x * V + e] = db[e];
+    for (int j = 0; j < W; ++j) {
+      const float2 v = unpack2(dw[j][e / 2]);
+      red[threadIdx.y][j][threadIdx.x * V + e] = e & 1 ? v.y : v.x;
+    }
+    const float2 v = unpack2(db[e / 2]);
+    red[threadIdx.y][W][threadIdx.x * V + e] = e & 1 ? v.y : v.x;
   }
   __syncthreads();
   float* pb = part + (long long)(b * NB + nb) * (W + 1) * D;
@@ -371,18 +450,19 @@ conv_step_kernel(const T* __restrict__ x, long long ldx, const float* __restrict
 #pragma unroll
   for (int j = 0; j < W - 1; ++j) rows[j].load(sb + (long long)j * D);
   rows[W - 1].load(x + b * ldx + c);
-  float tap[W][V], p[V];
-  load_taps<V, W>(w, bias, c, tap, p);
+  constexpr int P = kPairs<V>;
+  f32x2 tap[W][P], b0[P], win[W - 1][P], cur[P], p[P];
+  load_taps<V, W>(w, bias, c, tap, b0);
 #pragma unroll
-  for (int j = 0; j < W; ++j) {
-    float f[V];
-    rows[j].get(f);
-#pragma unroll
-    for (int e = 0; e < V; ++e) p[e] = fmaf(tap[j][e], f[e], p[e]);
-  }
+  for (int j = 0; j < W - 1; ++j) rows[j].get(win[j]);
+  rows[W - 1].get(cur);
+  taps_sum<V, W>(tap, b0, win, cur, p);
   if (SILU)
 #pragma unroll
-    for (int e = 0; e < V; ++e) p[e] = silu(p[e]);
+    for (int i = 0; i < P; ++i) {
+      const float2 v = unpack2(p[i]);
+      p[i] = pack2(silu(v.x), silu(v.y));
+    }
   Row<T, V> o;
   o.set(p);
   o.store(y + b * D + c);
@@ -392,18 +472,23 @@ conv_step_kernel(const T* __restrict__ x, long long ldx, const float* __restrict
 
 // ---------------------------------------------------------------- host side
 
-// Tokens that one thread walks.  Long walks read fewer rows twice; short
-// prompts need the threads more: 16 tokens where that still gives every SM
-// 1024 threads, else 4.
+// Tokens that one thread walks.  Long walks read fewer rows twice and load
+// their taps for more tokens; short prompts need the threads more.  32 tokens
+// where that still gives every SM 1024 threads (8 x 4096 x 2048 bf16, with
+// 256-thread blocks: 66 us with 32 and 64, 68 with 16), then 16, then 4.
 static int fwd_walk(long long B, int T, int CG) {
-  return B * ((T + 15) / 16) * CG >= 148LL * 1024 ? 16 : 4;
+  for (int L = 32; L > 4; L /= 2)
+    if (B * ((T + L - 1) / L) * CG >= 148LL * 1024) return L;
+  return 4;
 }
 
-// Tokens of one backward walk (a block runs kBY of them side by side): 32,
-// and 8 where 32 would leave SMs without a block.
+// Tokens of one backward walk (a block runs kBY of them side by side): 64
+// where that gives every SM four blocks (4 x 8192 x 2048 bf16: 108 us with 64,
+// 118 with 32), 32 where two, and 8 for less.
 static int bwd_walk(long long B, int T, int D, int V) {
   const long long cb = (D + kBX * V - 1) / (kBX * V);
-  return B * cb * ((T + 32 * kBY - 1) / (32 * kBY)) >= 2 * 148 ? 32 : 8;
+  auto blocks = [&](int L) { return B * cb * ((T + L * kBY - 1) / (L * kBY)); };
+  return blocks(64) >= 4 * 148 ? 64 : blocks(32) >= 2 * 148 ? 32 : 8;
 }
 
 static long long bwd_parts(int B, int T, int D, int V) {
@@ -416,10 +501,10 @@ static cudaError_t launch_fwd(const void* x, long long ldx, const float* w, cons
                               const void* s0, const int* lengths, void* y, void* sT, int B,
                               int Tn, int D, bool silu, cudaStream_t st) {
   const int CG = D / V, L = fwd_walk(B, Tn, CG), NB = (Tn + L - 1) / L;
-  const long long total = (long long)B * NB * CG, blocks = (total + 255) / 256;
+  const long long total = (long long)B * NB * CG, blocks = (total + kFT - 1) / kFT;
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
   auto k = silu ? conv_fwd_kernel<T, V, W, true> : conv_fwd_kernel<T, V, W, false>;
-  k<<<(unsigned)blocks, 256, 0, st>>>((const T*)x, ldx, w, bias, (const T*)s0, lengths, (T*)y,
+  k<<<(unsigned)blocks, kFT, 0, st>>>((const T*)x, ldx, w, bias, (const T*)s0, lengths, (T*)y,
                                       (T*)sT, Tn, D, CG, NB, L, total);
   return cudaGetLastError();
 }
@@ -505,7 +590,7 @@ kla_status kla_conv_fwd(const void* x, long long ldx, const float* w, const floa
   KLA_CONV_WIDTH(W, (e = launch_fwd<TY, V, KW>(x, ldx, w, bias, s0, lengths, y, sT, B, T, D, \
                                               silu != 0, st)))
   if (dtype == KLA_BF16) {
-    if (rows_aligned(x, D, ldx, 8, es)) { RUN(__nv_bfloat16, 8) } else { RUN(__nv_bfloat16, 1) }
+    if (rows_aligned(x, D, ldx, 4, es)) { RUN(__nv_bfloat16, 4) } else { RUN(__nv_bfloat16, 1) }
   } else {
     if (rows_aligned(x, D, ldx, 4, es)) { RUN(float, 4) } else { RUN(float, 1) }
   }
