@@ -12,10 +12,11 @@
 //
 // Bound by HBM: q and k read and written once (backward: gradients too).  A
 // row (one head of one token) lies on the smallest power of two of lanes that
-// gives each 8 channels; a block takes a few tokens with all their heads, so
-// that an angle's cosine and sine are formed once a token and shared by the
-// heads.  Angles are formed and reduced to [-pi, pi] in fp64 (a position of
-// 1e6 leaves 24-bit angles 0.06 off), their cosine and sine in fp32; norms
+// gives each 8 channels; a block takes a few tokens with all their heads.  A
+// thread stays with one token and walks through some of its heads, so that
+// cosines and sines are formed once a token and held in registers, and loads
+// the rows of several heads before it needs the first.  Angles are formed and reduced to [-pi, pi] in fp64 (a position of
+// 1e6 leaves 24-bit angles 0.06 off), their cosine and sine in fp32 (2^-21); norms
 // and products are fp32, and only the results are rounded, once.
 #include "kla_layer.cuh"
 
@@ -25,7 +26,7 @@ namespace qk {
 using namespace layer;
 
 constexpr int kNT = 256;
-constexpr int kTrig = 2048;  // angles a block holds
+constexpr int kTrig = 1024;  // angles of a block's tokens at most: kNT / LPR tokens, 4 LPR pairs
 
 struct Args {
   const void *q, *k, *gq, *gk;
@@ -41,24 +42,38 @@ struct Args {
   float eps, scale;
 };
 
+// Eight channels as they lie in memory.
 template <typename T>
-__device__ __forceinline__ void load8(const T* p, float (&f)[8]);
+struct Raw8;
 template <>
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&f)[8]) {
-  const uint4 r = *reinterpret_cast<const uint4*>(p);
-  const uint32_t u[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    f[2 * i] = __uint_as_float(u[i] << 16);
-    f[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+struct Raw8<__nv_bfloat16> {
+  uint4 r;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) {
+    r = *reinterpret_cast<const uint4*>(p);
   }
-}
+  __device__ __forceinline__ void zero() { r = make_uint4(0, 0, 0, 0); }
+  __device__ __forceinline__ void get(float (&f)[8]) const {
+    const uint32_t u[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f[2 * i] = __uint_as_float(u[i] << 16);
+      f[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+    }
+  }
+};
 template <>
-__device__ __forceinline__ void load8(const float* p, float (&f)[8]) {
-  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-  f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
-  f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
-}
+struct Raw8<float> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float* p) {
+    a = reinterpret_cast<const float4*>(p)[0];
+    b = reinterpret_cast<const float4*>(p)[1];
+  }
+  __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+  __device__ __forceinline__ void get(float (&f)[8]) const {
+    f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
+    f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+  }
+};
 template <typename T>
 __device__ __forceinline__ void store8(T* p, const float (&f)[8]);
 template <>
@@ -82,12 +97,12 @@ __device__ __forceinline__ void store8(float* p, const float (&f)[8]) {
 // SMEM through shared memory (any even rot).
 enum Reach { NONE = 0, PAIR = 1, LANE = 2, SMEM = 3 };
 
-// cos and sin of the block's tokens: s_cs[token][pair]
-__device__ __forceinline__ void make_angles(const Args& p, long long tok0, int nt,
-                                            float2* s_cs) {
+// Cosines and sines of the block's nt tokens, [token][pair], times scale.
+__device__ __forceinline__ void make_angles(const Args& p, long long tok0, int nt, float* s_cos,
+                                            float* s_sin) {
   const int np = p.rot / 2;
   for (int i = threadIdx.x; i < nt * np; i += kNT) {
-    const int tt = i / np, j = i % np;
+    const int tt = i / np, j = i - tt * np;
     const long long tok = tok0 + tt, b = tok / p.T;
     const int t = (int)(tok - b * p.T);
     const int at = p.pos ? p.pos[b * p.pos_stride + t] : p.pos0 + t;
@@ -95,141 +110,205 @@ __device__ __forceinline__ void make_angles(const Args& p, long long tok0, int n
     const double turns = rint(ang * 0.15915494309189535);  // 1 / 2 pi
     const float r = (float)fma(-turns, 6.283185307179586, ang);
     float s, c;
-    sincosf(r, &s, &c);
-    s_cs[i] = make_float2(c * p.scale, s * p.scale);
+    __sincosf(r, &s, &c);  // within 2^-21 on [-pi, pi]
+    s_cos[i] = c * p.scale;
+    s_sin[i] = s * p.scale;
   }
 }
 
-// v (this lane's 8 channels from c) turned by the token's angles; SIGN -1
-// turns back.  row: this row's staging of d floats (SMEM).
+// This lane's part of its token's angles: co[e], si[e] are what channel c + e
+// and its partner are multiplied with (PAIR: one of each for two channels).
+// Channels that are not turned get (1, 0).
 template <int REACH>
-__device__ __forceinline__ void turn(float (&v)[8], const Args& p, int c, const float2* cs,
-                                     float* row, float sign) {
-  if constexpr (REACH == PAIR) {
-#pragma unroll
-    for (int e = 0; e < 8; e += 2)
-      if (c + e < p.rot) {
-        const float2 t = cs[(c + e) >> 1];
-        const float a = v[e], b = v[e + 1], s = sign * t.y;
-        v[e] = a * t.x - b * s;
-        v[e + 1] = fmaf(b, t.x, a * s);
-      }
-  } else if constexpr (REACH == LANE) {
-    const int half = p.rot / 2;
-    const bool lo = c < half, in = c < p.rot;
-    const int dist = half / 8, lane = threadIdx.x & 31;
-    const int from = in ? (lo ? lane + dist : lane - dist) : lane;
-    const int base = lo ? c : c - half;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float o = __shfl_sync(0xffffffffu, v[e], from);
-      if (in) {
-        const float2 t = cs[base + e];
-        const float s = lo ? -sign * t.y : sign * t.y;
-        v[e] = fmaf(v[e], t.x, o * s);
-      }
-    }
-  } else if constexpr (REACH == SMEM) {
-    const int half = p.rot / 2;
-    if (c < p.d)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) row[c + e] = v[e];
-    __syncwarp();
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int i = c + e;
-      if (i < p.rot) {
-        const bool lo = i < half;
-        const float2 t = cs[lo ? i : i - half];
-        const float o = row[lo ? i + half : i - half];
-        v[e] = fmaf(v[e], t.x, o * (lo ? -sign * t.y : sign * t.y));
-      }
-    }
-    __syncwarp();
-  }
-}
+struct Turn {
+  static constexpr int M = REACH == PAIR ? 4 : 8;
+  float co[M], si[M];
+  int from;  // LANE: the partner's lane
 
-// LPR lanes a row.  BWD: q and k with their gradients to dq, dk, and the
-// weights' parts.
+  __device__ __forceinline__ void load(const Args& p, int c, const float* cosv,
+                                       const float* sinv) {
+    const int half = p.rot / 2, lane = threadIdx.x & 31;
+    from = lane;
+#pragma unroll
+    for (int e = 0; e < M; ++e) { co[e] = 1.f; si[e] = 0.f; }
+    if constexpr (REACH == PAIR) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (c + 2 * e < p.rot) {
+          co[e] = cosv[c / 2 + e];
+          si[e] = sinv[c / 2 + e];
+        }
+    } else {
+      if constexpr (REACH == LANE) {
+        if (c < p.rot) from = c < half ? lane + half / 8 : lane - half / 8;
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int i = c + e;
+        if (i < p.rot) {
+          co[e] = cosv[i < half ? i : i - half];
+          si[e] = i < half ? -sinv[i] : sinv[i - half];
+        }
+      }
+    }
+  }
+
+  // v turned (SIGN 1) or turned back (SIGN -1); row: d floats of staging (SMEM)
+  template <int SIGN>
+  __device__ __forceinline__ void apply(float (&v)[8], const Args& p, int c, float* row) const {
+    if constexpr (REACH == PAIR) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float a = v[2 * e], b = v[2 * e + 1], s = SIGN * si[e];
+        v[2 * e] = fmaf(a, co[e], -b * s);
+        v[2 * e + 1] = fmaf(b, co[e], a * s);
+      }
+    } else if constexpr (REACH == LANE) {
+      float o[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) o[e] = __shfl_sync(0xffffffffu, v[e], from);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = fmaf(v[e], co[e], o[e] * (SIGN * si[e]));
+    } else if constexpr (REACH == SMEM) {
+      const int half = p.rot / 2;
+      if (c < p.d)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) row[c + e] = v[e];
+      __syncwarp();
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int i = c + e;
+        if (i < p.rot)
+          v[e] = fmaf(v[e], co[e], row[i < half ? i + half : i - half] * (SIGN * si[e]));
+      }
+      __syncwarp();
+    }
+  }
+};
+template <>
+struct Turn<NONE> {
+  __device__ __forceinline__ void load(const Args&, int, const float*, const float*) {}
+  template <int SIGN>
+  __device__ __forceinline__ void apply(float (&)[8], const Args&, int, float*) const {}
+};
+
+// LPR lanes a row; a block has kNT / LPR row places, TB tokens of them with
+// the same number of places each.  BWD: q and k with their gradients to dq,
+// dk, and the weights' parts.
 template <typename T, int LPR, int REACH, bool BWD>
-__global__ void __launch_bounds__(kNT)
+__global__ void __launch_bounds__(kNT, BWD ? 2 : 4)
 qk_kernel(Args p, long long ntiles) {
-  constexpr int RPB = kNT / LPR;  // rows in flight
-  __shared__ float2 s_cs[REACH == NONE ? 1 : kTrig];
+  constexpr int RPB = kNT / LPR;
+  constexpr int U = BWD || sizeof(T) == 4 ? 2 : 4;  // rows loaded ahead
+  __shared__ __align__(16) float s_cos[REACH == NONE ? 1 : kTrig];
+  __shared__ __align__(16) float s_sin[REACH == NONE ? 1 : kTrig];
   __shared__ float s_row[REACH == SMEM ? RPB : 1][REACH == SMEM ? LPR * 8 : 1];
   const int lr = threadIdx.x % LPR, rr = threadIdx.x / LPR, c = lr * 8;
-  const bool in = c < p.d;
+  const int places = RPB / p.TB;  // of a token
+  const int tt = rr / places, h0 = rr - tt * places;
   const int H = p.Hq + p.Hk;
   const float inv_m = p.norm == 2 ? 1.f / (float)p.d : 1.f;
-  float wq[8], wk[8], aq[8] = {}, ak[8] = {};
-#pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    wq[e] = in && p.wq ? p.wq[c + e] : 1.f;
-    wk[e] = in && p.wk ? p.wk[c + e] : 1.f;
+  float* const row = s_row[REACH == SMEM ? rr : 0];
+  float aq[BWD ? 8 : 1] = {}, ak[BWD ? 8 : 1] = {};
+  __shared__ __align__(16) float s_w[2][LPR * 8];
+  const bool weighted = p.wq || p.wk;
+  if (weighted) {
+    for (int i = threadIdx.x; i < LPR * 8; i += kNT) {
+      s_w[0][i] = i < p.d && p.wq ? p.wq[i] : 1.f;
+      s_w[1][i] = i < p.d && p.wk ? p.wk[i] : 1.f;
+    }
+    __syncthreads();
   }
+  auto times_w = [&](float (&v)[8], bool isq) {
+    if (!weighted) return;
+    const float4* w = reinterpret_cast<const float4*>(&s_w[isq ? 0 : 1][c]);
+    const float4 a = w[0], b = w[1];
+    v[0] *= a.x; v[1] *= a.y; v[2] *= a.z; v[3] *= a.w;
+    v[4] *= b.x; v[5] *= b.y; v[6] *= b.z; v[7] *= b.w;
+  };
   for (long long tile = blockIdx.x; tile < ntiles; tile += gridDim.x) {
-    const long long tok0 = tile * p.TB;
+    const long long tok0 = tile * p.TB, tok = tok0 + tt;
     const int nt = (int)min((long long)p.TB, p.tokens - tok0);
+    const bool mine = c < p.d && tt < nt;
+    Raw8<T> x[U], g[BWD ? U : 1];
+    auto load = [&](int h) {  // heads h, h + places, ...
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        const int hh = h + i * places;
+        x[i].zero();
+        if (BWD) g[i].zero();
+        if (mine && hh < H) {
+          const bool isq = hh < p.Hq;
+          const int k = isq ? hh : hh - p.Hq;
+          x[i].load((isq ? (const T*)p.q + tok * p.ldq : (const T*)p.k + tok * p.ldk) +
+                    (long long)k * p.d + c);
+          if (BWD)
+            g[i].load((isq ? (const T*)p.gq + tok * p.Hq * p.d
+                           : (const T*)p.gk + tok * p.Hk * p.d) +
+                      (long long)k * p.d + c);
+        }
+      }
+    };
+    load(h0);
+    Turn<REACH> turn;
     if constexpr (REACH != NONE) {
       if (tile != blockIdx.x) __syncthreads();  // the last tile's angles are read
-      make_angles(p, tok0, nt, s_cs);
+      make_angles(p, tok0, nt, s_cos, s_sin);
       __syncthreads();
+      const int at = tt < nt ? tt * (p.rot / 2) : 0;
+      turn.load(p, c, s_cos + at, s_sin + at);
     }
-    const int nrow = nt * H;
-    // whole warps run every pass: lanes without a row take part in shuffles
-    for (int r0 = 0; r0 < nrow; r0 += RPB) {
-      const int r = r0 + rr;
-      const bool live = in && r < nrow;
-      const int tt = r < nrow ? r / H : 0, hh = r < nrow ? r - tt * H : 0;
-      const long long tok = tok0 + tt;
-      const bool isq = hh < p.Hq;
-      const T* src = isq ? (const T*)p.q + tok * p.ldq + hh * p.d
-                         : (const T*)p.k + tok * p.ldk + (hh - p.Hq) * p.d;
-      const long long at = isq ? (tok * p.Hq + hh) * p.d : (tok * p.Hk + hh - p.Hq) * p.d;
-      float x[8] = {}, g[8] = {};
-      if (live) {
-        load8(src + c, x);
-        if (BWD) load8((isq ? (const T*)p.gq : (const T*)p.gk) + at + c, g);
-      }
-      float rs = 1.f;
-      if (p.norm) {
-        float ss = 0.f;
+    // every thread makes as many passes: all lanes take part in the exchanges
+    for (int hb = 0; hb < H; hb += U * places) {
+      if (hb > 0) load(hb + h0);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
-#pragma unroll
-        for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        rs = 1.f / sqrtf(fmaf(ss, inv_m, p.eps));
-      }
-      const float2* cs = s_cs + (REACH == NONE ? 0 : tt * (p.rot / 2));
-      float* row = s_row[REACH == SMEM ? rr : 0];
-      if constexpr (!BWD) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] *= rs * (isq ? wq[e] : wk[e]);
-        turn<REACH>(x, p, c, cs, row, 1.f);
-        if (live) store8((isq ? (T*)p.oq : (T*)p.ok) + at + c, x);
-      } else {
-        turn<REACH>(g, p, c, cs, row, -1.f);
-        float dot = 0.f;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          x[e] *= rs;
-          if (live) {
-            if (isq)
-              aq[e] = fmaf(g[e], x[e], aq[e]);
-            else
-              ak[e] = fmaf(g[e], x[e], ak[e]);
-          }
-          g[e] *= isq ? wq[e] : wk[e];
-          dot = fmaf(g[e], x[e], dot);
-        }
+      for (int i = 0; i < U; ++i) {
+        if (hb + i * places >= H) break;  // the same for all threads
+        const int hh = hb + i * places + h0;
+        const bool live = mine && hh < H, isq = hh < p.Hq;
+        const long long at =
+            (isq ? (tok * p.Hq + hh) : (tok * p.Hk + hh - p.Hq)) * p.d + c;
+        float v[8], r = 1.f;
+        x[i].get(v);
         if (p.norm) {
+          float ss = 0.f;
 #pragma unroll
-          for (int o = LPR / 2; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
-          dot *= inv_m;
+          for (int e = 0; e < 8; ++e) ss = fmaf(v[e], v[e], ss);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) g[e] = rs * fmaf(-x[e], dot, g[e]);
+          for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+          r = rsqrtf(fmaf(ss, inv_m, p.eps));
         }
-        if (live) store8((isq ? (T*)p.oq : (T*)p.ok) + at + c, g);
+        if constexpr (!BWD) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[e] *= r;
+          times_w(v, isq);
+          turn.template apply<1>(v, p, c, row);
+          if (live) store8((isq ? (T*)p.oq : (T*)p.ok) + at, v);
+        } else {
+          float d[8];
+          g[i].get(d);
+          turn.template apply<-1>(d, p, c, row);
+          float dot = 0.f;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            v[e] *= r;
+            if (isq)
+              aq[e] = fmaf(d[e], v[e], aq[e]);
+            else
+              ak[e] = fmaf(d[e], v[e], ak[e]);
+          }
+          times_w(d, isq);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) dot = fmaf(d[e], v[e], dot);
+          if (p.norm) {
+#pragma unroll
+            for (int o = LPR / 2; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+            dot *= inv_m;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) d[e] = r * fmaf(-v[e], dot, d[e]);
+          }
+          if (live) store8((isq ? (T*)p.oq : (T*)p.ok) + at, d);
+        }
       }
     }
   }
@@ -246,7 +325,7 @@ qk_kernel(Args p, long long ntiles) {
       for (int i = threadIdx.x; i < p.d; i += kNT) {
         float s = 0.f;
 #pragma unroll 8
-        for (int r = 0; r < RPB; ++r) s += s_sum[r][i];
+        for (int j = 0; j < RPB; ++j) s += s_sum[j][i];
         p.part[((long long)blockIdx.x * 2 + w) * p.d + i] = s;
       }
     }
@@ -285,15 +364,15 @@ static int lanes(int d) {
   return l;
 }
 
-// Tokens of a block: four passes of its rows, within its store of angles.
-static int tokens_per_block(int H, int d, int rot, long long tokens) {
-  const int rows = 4 * (kNT / lanes(d));
-  long long tb = rows / H;
-  const long long most = rot ? kTrig / (rot / 2) : tb;
-  if (tb > most) tb = most;
-  // few tokens: one each, so that every SM has work
-  if (tokens < 148 * tb) tb = (tokens + 147) / 148;
-  return (int)(tb < 1 ? 1 : tb);
+// Tokens of a block, a power of two: a quarter of a token's heads side by side,
+// so that a thread uses its angles for about four, and all of them (up to the
+// block's places) while the blocks would not give every SM two.
+static int tokens_per_block(int H, int d, long long tokens) {
+  const int places = kNT / lanes(d);
+  int side = 1;
+  while (side * 8 <= H && side < places) side *= 2;
+  while (side < H && side < places && tokens < 2LL * 148 * (places / side)) side *= 2;
+  return places / side;
 }
 
 static long long blocks_of(long long tokens, int TB, bool bwd) {
@@ -315,7 +394,7 @@ static void launch_reach(const Args& a, int reach, unsigned grid, long long ntil
 
 template <typename T, bool BWD>
 static cudaError_t launch(Args a, cudaStream_t st) {
-  a.TB = tokens_per_block(a.Hq + a.Hk, a.d, a.rot, a.tokens);
+  a.TB = tokens_per_block(a.Hq + a.Hk, a.d, a.tokens);
   const long long ntiles = (a.tokens + a.TB - 1) / a.TB;
   const unsigned grid = (unsigned)blocks_of(a.tokens, a.TB, BWD);
   const int reach = a.rot == 0 ? NONE : a.interleaved ? PAIR : a.rot % 16 == 0 ? LANE : SMEM;
@@ -346,8 +425,8 @@ static kla_status check(int B, int T, int Hq, int Hk, int d, int rot, int norm, 
   return KLA_OK;
 }
 
-static long long parts_of(long long tokens, int H, int d, int rot) {
-  return tokens == 0 ? 0 : blocks_of(tokens, tokens_per_block(H, d, rot, tokens), true);
+static long long parts_of(long long tokens, int H, int d) {
+  return tokens == 0 ? 0 : blocks_of(tokens, tokens_per_block(H, d, tokens), true);
 }
 
 }  // namespace qk
@@ -395,7 +474,7 @@ size_t kla_qk_norm_bwd_workspace_size(int B, int T, int Hq, int Hk, int d, int r
   if (check(B, T, Hq, Hk, d, rot, 0, 0.f, 1.f, (long long)Hq * d, (long long)Hk * d, KLA_BF16) !=
       KLA_OK)
     return 0;
-  return (size_t)parts_of((long long)B * T, Hq + Hk, d, rot) * 2 * d * sizeof(float);
+  return (size_t)parts_of((long long)B * T, Hq + Hk, d) * 2 * d * sizeof(float);
 }
 
 kla_status kla_qk_norm_bwd(const void* q, const void* k, long long ldq, long long ldk,
@@ -444,7 +523,7 @@ kla_status kla_qk_norm_bwd(const void* q, const void* k, long long ldq, long lon
   a.interleaved = interleaved != 0; a.eps = eps; a.scale = scale;
   e = dtype == KLA_BF16 ? launch<__nv_bfloat16, true>(a, st) : launch<float, true>(a, st);
   if (e == cudaSuccess && weights) {
-    const int P = (int)parts_of(rows, Hq + Hk, d, rot);
+    const int P = (int)parts_of(rows, Hq + Hk, d);
     qk_reduce_kernel<<<(unsigned)((2 * d + 31) / 32), 1024, 0, st>>>(a.part, P, d, grad_wq,
                                                                      grad_wk);
     e = cudaGetLastError();
