@@ -100,12 +100,14 @@ enum Reach { NONE = 0, PAIR = 1, LANE = 2, SMEM = 3 };
 // Cosines and sines of the block's nt tokens, [token][pair], times scale.
 __device__ __forceinline__ void make_angles(const Args& p, long long tok0, int nt, float* s_cos,
                                             float* s_sin) {
-  const int np = p.rot / 2;
-  for (int i = threadIdx.x; i < nt * np; i += kNT) {
-    const int tt = i / np, j = i - tt * np;
-    const long long tok = tok0 + tt, b = tok / p.T;
-    const int t = (int)(tok - b * p.T);
-    const int at = p.pos ? p.pos[b * p.pos_stride + t] : p.pos0 + t;
+  const unsigned np = p.rot / 2;
+  const long long b0 = tok0 / p.T;
+  const unsigned first = (unsigned)(tok0 - b0 * p.T);
+  for (unsigned i = threadIdx.x; i < nt * np; i += kNT) {
+    const unsigned tt = i / np, j = i - tt * np;
+    // first + tt < 2^30 + kNT
+    const unsigned more = (first + tt) / (unsigned)p.T, t = first + tt - more * (unsigned)p.T;
+    const int at = p.pos ? p.pos[(b0 + more) * p.pos_stride + t] : p.pos0 + (int)t;
     const double ang = (double)at * (double)p.inv_freq[j];
     const double turns = rint(ang * 0.15915494309189535);  // 1 / 2 pi
     const float r = (float)fma(-turns, 6.283185307179586, ang);
@@ -231,6 +233,17 @@ qk_kernel(Args p, long long ntiles) {
     const int nt = (int)min((long long)p.TB, p.tokens - tok0);
     const bool mine = c < p.d && tt < nt;
     Raw8<T> x[U], g[BWD ? U : 1];
+    // this token's rows, in bytes from each array's start: head h of q, or head
+    // h - Hq of k, lies h * d elements on (k's starts are set back by Hq heads)
+    constexpr long long es = sizeof(T);
+    const long long back = (long long)p.Hq * p.d;
+    const long long q_in = (tok * p.ldq + c) * es, k_in = (tok * p.ldk + c - back) * es;
+    const long long q_out = (tok * p.Hq * p.d + c) * es;
+    const long long k_out = (tok * p.Hk * p.d + c - back) * es;
+    auto at = [&](const void* q, const void* k, long long qo, long long ko, int h) {
+      const char* a = h < p.Hq ? (const char*)q + qo : (const char*)k + ko;
+      return (T*)(a + (long long)(h * p.d) * es);
+    };
     auto load = [&](int h) {  // heads h, h + places, ...
 #pragma unroll
       for (int i = 0; i < U; ++i) {
@@ -238,14 +251,8 @@ qk_kernel(Args p, long long ntiles) {
         x[i].zero();
         if (BWD) g[i].zero();
         if (mine && hh < H) {
-          const bool isq = hh < p.Hq;
-          const int k = isq ? hh : hh - p.Hq;
-          x[i].load((isq ? (const T*)p.q + tok * p.ldq : (const T*)p.k + tok * p.ldk) +
-                    (long long)k * p.d + c);
-          if (BWD)
-            g[i].load((isq ? (const T*)p.gq + tok * p.Hq * p.d
-                           : (const T*)p.gk + tok * p.Hk * p.d) +
-                      (long long)k * p.d + c);
+          x[i].load(at(p.q, p.k, q_in, k_in, hh));
+          if (BWD) g[i].load(at(p.gq, p.gk, q_out, k_out, hh));
         }
       }
     };
@@ -255,8 +262,8 @@ qk_kernel(Args p, long long ntiles) {
       if (tile != blockIdx.x) __syncthreads();  // the last tile's angles are read
       make_angles(p, tok0, nt, s_cos, s_sin);
       __syncthreads();
-      const int at = tt < nt ? tt * (p.rot / 2) : 0;
-      turn.load(p, c, s_cos + at, s_sin + at);
+      const int mine_at = tt < nt ? tt * (p.rot / 2) : 0;
+      turn.load(p, c, s_cos + mine_at, s_sin + mine_at);
     }
     // every thread makes as many passes: all lanes take part in the exchanges
     for (int hb = 0; hb < H; hb += U * places) {
@@ -266,8 +273,6 @@ qk_kernel(Args p, long long ntiles) {
         if (hb + i * places >= H) break;  // the same for all threads
         const int hh = hb + i * places + h0;
         const bool live = mine && hh < H, isq = hh < p.Hq;
-        const long long at =
-            (isq ? (tok * p.Hq + hh) : (tok * p.Hk + hh - p.Hq)) * p.d + c;
         float v[8], r = 1.f;
         x[i].get(v);
         if (p.norm) {
@@ -283,7 +288,7 @@ qk_kernel(Args p, long long ntiles) {
           for (int e = 0; e < 8; ++e) v[e] *= r;
           times_w(v, isq);
           turn.template apply<1>(v, p, c, row);
-          if (live) store8((isq ? (T*)p.oq : (T*)p.ok) + at, v);
+          if (live) store8(at(p.oq, p.ok, q_out, k_out, hh), v);
         } else {
           float d[8];
           g[i].get(d);
@@ -307,7 +312,7 @@ qk_kernel(Args p, long long ntiles) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) d[e] = r * fmaf(-v[e], dot, d[e]);
           }
-          if (live) store8((isq ? (T*)p.oq : (T*)p.ok) + at, d);
+          if (live) store8(at(p.oq, p.ok, q_out, k_out, hh), d);
         }
       }
     }
