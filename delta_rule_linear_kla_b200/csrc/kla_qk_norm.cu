@@ -228,35 +228,47 @@ qk_kernel(Args p, long long ntiles) {
     v[0] *= a.x; v[1] *= a.y; v[2] *= a.z; v[3] *= a.w;
     v[4] *= b.x; v[5] *= b.y; v[6] *= b.z; v[7] *= b.w;
   };
-  for (long long tile = blockIdx.x; tile < ntiles; tile += gridDim.x) {
-    const long long tok0 = tile * p.TB, tok = tok0 + tt;
-    const int nt = (int)min((long long)p.TB, p.tokens - tok0);
-    const bool mine = c < p.d && tt < nt;
-    Raw8<T> x[U], g[BWD ? U : 1];
-    // this token's rows, in bytes from each array's start: head h of q, or head
-    // h - Hq of k, lies h * d elements on (k's starts are set back by Hq heads)
-    constexpr long long es = sizeof(T);
-    const long long back = (long long)p.Hq * p.d;
-    const long long q_in = (tok * p.ldq + c) * es, k_in = (tok * p.ldk + c - back) * es;
-    const long long q_out = (tok * p.Hq * p.d + c) * es;
-    const long long k_out = (tok * p.Hk * p.d + c - back) * es;
-    auto at = [&](const void* q, const void* k, long long qo, long long ko, int h) {
-      const char* a = h < p.Hq ? (const char*)q + qo : (const char*)k + ko;
-      return (T*)(a + (long long)(h * p.d) * es);
-    };
-    auto load = [&](int h) {  // heads h, h + places, ...
+  // a token's rows, in bytes from each array's start: head h of q, or head h -
+  // Hq of k, lies h * d elements on (k's starts are set back by Hq heads)
+  constexpr long long es = sizeof(T);
+  const long long back = (long long)p.Hq * p.d;
+  struct Where {
+    long long q_in, k_in, q_out, k_out;
+    bool mine;
+  };
+  auto where = [&](long long tile) {
+    const long long tok = tile * p.TB + tt;
+    Where w;
+    w.q_in = (tok * p.ldq + c) * es;
+    w.k_in = (tok * p.ldk + c - back) * es;
+    w.q_out = (tok * p.Hq * p.d + c) * es;
+    w.k_out = (tok * p.Hk * p.d + c - back) * es;
+    w.mine = c < p.d && tile < ntiles && tok < p.tokens;
+    return w;
+  };
+  auto at = [&](const void* q, const void* k, long long qo, long long ko, int h) {
+    const char* a = h < p.Hq ? (const char*)q + qo : (const char*)k + ko;
+    return (T*)(a + (long long)(h * p.d) * es);
+  };
+  Raw8<T> xn[U], gn[BWD ? U : 1];  // the rows to come
+  auto load = [&](const Where& w, int hb) {  // heads hb + h0, one place apart
 #pragma unroll
-      for (int i = 0; i < U; ++i) {
-        const int hh = h + i * places;
-        x[i].zero();
-        if (BWD) g[i].zero();
-        if (mine && hh < H) {
-          x[i].load(at(p.q, p.k, q_in, k_in, hh));
-          if (BWD) g[i].load(at(p.gq, p.gk, q_out, k_out, hh));
-        }
+    for (int i = 0; i < U; ++i) {
+      const int hh = hb + i * places + h0;
+      xn[i].zero();
+      if (BWD) gn[i].zero();
+      if (w.mine && hh < H) {
+        xn[i].load(at(p.q, p.k, w.q_in, w.k_in, hh));
+        if (BWD) gn[i].load(at(p.gq, p.gk, w.q_out, w.k_out, hh));
       }
-    };
-    load(h0);
+    }
+  };
+  Where w = where(blockIdx.x);
+  load(w, 0);
+  for (long long tile = blockIdx.x; tile < ntiles; tile += gridDim.x) {  // forward: once
+    const long long tok0 = tile * p.TB;
+    const int nt = (int)min((long long)p.TB, p.tokens - tok0);
+    const Where wn = where(tile + gridDim.x);
     Turn<REACH> turn;
     if constexpr (REACH != NONE) {
       if (tile != blockIdx.x) __syncthreads();  // the last tile's angles are read
@@ -267,12 +279,26 @@ qk_kernel(Args p, long long ntiles) {
     }
     // every thread makes as many passes: all lanes take part in the exchanges
     for (int hb = 0; hb < H; hb += U * places) {
-      if (hb > 0) load(hb + h0);
+      // forward: four blocks an SM cover the loads; backward: two, so the rows
+      // of the next pass (or tile) are on their way during this one
+      if (!BWD && hb > 0) load(w, hb);
+      Raw8<T> x[U], g[BWD ? U : 1];
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        x[i] = xn[i];
+        if (BWD) g[i] = gn[i];
+      }
+      if (BWD) {
+        if (hb + U * places < H)
+          load(w, hb + U * places);
+        else
+          load(wn, 0);
+      }
 #pragma unroll
       for (int i = 0; i < U; ++i) {
         if (hb + i * places >= H) break;  // the same for all threads
         const int hh = hb + i * places + h0;
-        const bool live = mine && hh < H, isq = hh < p.Hq;
+        const bool live = w.mine && hh < H, isq = hh < p.Hq;
         float v[8], r = 1.f;
         x[i].get(v);
         if (p.norm) {
@@ -288,7 +314,7 @@ qk_kernel(Args p, long long ntiles) {
           for (int e = 0; e < 8; ++e) v[e] *= r;
           times_w(v, isq);
           turn.template apply<1>(v, p, c, row);
-          if (live) store8(at(p.oq, p.ok, q_out, k_out, hh), v);
+          if (live) store8(at(p.oq, p.ok, w.q_out, w.k_out, hh), v);
         } else {
           float d[8];
           g[i].get(d);
@@ -312,10 +338,11 @@ qk_kernel(Args p, long long ntiles) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) d[e] = r * fmaf(-v[e], dot, d[e]);
           }
-          if (live) store8(at(p.oq, p.ok, q_out, k_out, hh), d);
+          if (live) store8(at(p.oq, p.ok, w.q_out, w.k_out, hh), d);
         }
       }
     }
+    if (BWD) w = wn;
   }
   if constexpr (BWD) {
     if (!p.part) return;
