@@ -598,6 +598,11 @@ def kda_decode_step_beta(q, k, v, g, beta, S, *, o=None, stream=None):
 # Layer operators around the recurrences: short causal convolution, selective
 # state space scan, norm and rotation of queries and keys.
 
+# handle of a device's current stream, without the Stream object around it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 class _On:
     """_on for calls of a few microseconds: no context is entered when the
     tensors' device and its current stream are the ones to use anyway."""
@@ -609,7 +614,7 @@ class _On:
 
     def __enter__(self):
         if self.stream is None and torch.cuda.current_device() == self.dev.index:
-            return torch.cuda.current_stream(self.dev).cuda_stream
+            return _raw_stream(self.dev.index)
         self.ctx = contextlib.ExitStack()
         with contextlib.ExitStack() as stack:
             stack.enter_context(torch.cuda.device(self.dev))
@@ -625,6 +630,17 @@ class _On:
             self.ctx.close()
 
 
+def _p(t, name, dtype, shape, dev):
+    """Address of a contiguous argument (None stays None); _need's checks, and
+    its words where one fails."""
+    if t is None:
+        return None
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.device == dev
+            and t.shape == shape and t.is_contiguous()):
+        _need(t, name, dtype, shape, dev)
+    return t.data_ptr()
+
+
 def _rows(t, name, dtype, lead, inner, dev):
     """Elements between the rows of an input that may be rows of a wider
     matrix: shape lead + inner, inner contiguous, rows evenly spaced."""
@@ -632,32 +648,29 @@ def _rows(t, name, dtype, lead, inner, dev):
         raise ValueError("%s must be a CUDA tensor" % name)
     if t.device != dev:
         raise ValueError("%s is on %s, the call's other tensors on %s" % (name, t.device, dev))
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise ValueError("%s must be %s, got %s" % (name, dtype, t.dtype))
-    if t.shape != lead + inner:
-        raise ValueError("%s must have shape %s, got %s"
-                         % (name, tuple(lead + inner), tuple(t.shape)))
-    n = 1
-    for m in inner:
-        n *= m
-    if t.numel() == 0 or t.is_contiguous():
+    shape = lead + inner
+    if t.shape != shape:
+        raise ValueError("%s must have shape %s, got %s" % (name, shape, tuple(t.shape)))
+    n = inner[0] if len(inner) == 1 else inner[0] * inner[1]
+    if t.is_contiguous() or t.numel() == 0:
         return n
     st, want = t.stride(), 1
-    for i in range(len(t.shape) - 1, len(lead) - 1, -1):
-        if t.shape[i] != 1 and st[i] != want:
+    for i in range(len(shape) - 1, len(lead) - 1, -1):
+        if st[i] != want and shape[i] != 1:
             raise ValueError("%s: the elements of a row must be contiguous" % name)
-        want *= t.shape[i]
-    ld = None
-    span = 1
+        want *= shape[i]
+    ld, span = None, 1
     for i in range(len(lead) - 1, -1, -1):
         if lead[i] != 1:
             if ld is None:
-                ld = st[i] // span  # span is 1, or the rows before are single
+                ld = st[i]  # the rows before are single
                 if ld < n:
                     raise ValueError("%s: rows must not overlap" % name)
             if st[i] != ld * span:
                 raise ValueError("%s: rows must be evenly spaced" % name)
-        span *= lead[i]
+            span *= lead[i]
     return n if ld is None else ld
 
 
@@ -688,16 +701,17 @@ def conv_bwd_workspace_size(B: int, T: int, D: int, W: int) -> int:
 
 
 def _conv_args(x, w, bias, s0, lengths, lead):
+    """Sizes, x's row pitch and the addresses of x .. lengths."""
     dt, dev = x.dtype, x.device
     D = x.shape[-1]
-    _need(w, "w", torch.float32, dev=dev)
-    if w is None or w.dim() != 2 or w.shape[0] != D:
+    if not isinstance(w, torch.Tensor) or w.dim() != 2 or w.shape[0] != D:
         raise ValueError("w must be a [D, W] CUDA tensor with D = %d" % D)
     W = w.shape[1]
-    _need(bias, "bias", torch.float32, (D,), dev)
-    _need(s0, "s0", dt, (lead[0], W - 1, D), dev)
-    _need(lengths, "lengths", torch.int32, (lead[0],), dev)
-    return D, W, _rows(x, "x", dt, lead, (D,), dev)
+    ldx = _rows(x, "x", dt, lead, (D,), dev)
+    return D, W, (x.data_ptr(), ldx, _p(w, "w", torch.float32, (D, W), dev),
+                  _p(bias, "bias", torch.float32, (D,), dev),
+                  _p(s0, "s0", dt, (lead[0], W - 1, D), dev),
+                  _p(lengths, "lengths", torch.int32, (lead[0],), dev))
 
 
 def conv_fwd(x, w, bias=None, s0=None, *, silu: bool = True, lengths=None, y=None, sT=None,
@@ -709,15 +723,13 @@ def conv_fwd(x, w, bias=None, s0=None, *, silu: bool = True, lengths=None, y=Non
     dt, dev = _act(x), x.device
     B, T, _ = _dims(x, "x", 3)
     with _On(x, stream) as s:
-        D, W, ldx = _conv_args(x, w, bias, s0, lengths, (B, T))
+        D, W, args = _conv_args(x, w, bias, s0, lengths, (B, T))
         if y is None:
             y = torch.empty((B, T, D), dtype=dt, device=dev)
-        _need(y, "y", dt, (B, T, D), dev)
         if sT is None and return_state:
             sT = torch.empty((B, W - 1, D), dtype=dt, device=dev)
-        _need(sT, "sT", dt, (B, W - 1, D), dev)
         st = _native.lib().kla_conv_fwd(
-            _ptr(x), ldx, _ptr(w), _ptr(bias), _ptr(s0), _ptr(lengths), _ptr(y), _ptr(sT),
+            *args, _p(y, "y", dt, (B, T, D), dev), _p(sT, "sT", dt, (B, W - 1, D), dev),
             B, T, D, W, bool(silu), _DT[dt], s)
     _check(st, "kla_conv_fwd")
     return y, sT
@@ -730,11 +742,11 @@ def conv_bwd(x, w, grad_y, bias=None, s0=None, grad_sT=None, *, silu: bool = Tru
     unless need_s0), dw and dbias fp32 (dbias None without a bias)."""
     dt, dev = _act(x), x.device
     B, T, _ = _dims(x, "x", 3)
+    _need_all(grad_y, "grad_y")
     with _On(x, stream) as s:
-        D, W, ldx = _conv_args(x, w, bias, s0, lengths, (B, T))
-        _need_all(grad_y, "grad_y")
-        _need(grad_y, "grad_y", dt, (B, T, D), dev)
-        _need(grad_sT, "grad_sT", dt, (B, W - 1, D), dev)
+        D, W, args = _conv_args(x, w, bias, s0, lengths, (B, T))
+        pg = _p(grad_y, "grad_y", dt, (B, T, D), dev)
+        ps = _p(grad_sT, "grad_sT", dt, (B, W - 1, D), dev)
         f32 = dict(dtype=torch.float32, device=dev)
         out = dict(dx=torch.empty((B, T, D), dtype=dt, device=dev),
                    dw=torch.empty((D, W), **f32),
@@ -742,8 +754,7 @@ def conv_bwd(x, w, grad_y, bias=None, s0=None, grad_sT=None, *, silu: bool = Tru
                    ds0=torch.empty((B, W - 1, D), dtype=dt, device=dev) if need_s0 else None)
         workspace, nws = _scratch(workspace, conv_bwd_workspace_size(B, T, D, W), dev)
         st = _native.lib().kla_conv_bwd(
-            _ptr(x), ldx, _ptr(w), _ptr(bias), _ptr(s0), _ptr(lengths), _ptr(grad_y),
-            _ptr(grad_sT), _ptr(out["dx"]), _ptr(out["dw"]), _ptr(out["dbias"]),
+            *args, pg, ps, _ptr(out["dx"]), _ptr(out["dw"]), _ptr(out["dbias"]),
             _ptr(out["ds0"]), B, T, D, W, bool(silu), _DT[dt], _ptr(workspace), nws, s)
     _check(st, "kla_conv_bwd")
     return out
@@ -755,15 +766,13 @@ def conv_step(x, w, state, bias=None, *, silu: bool = True, y=None, stream=None)
     [B,D]."""
     dt, dev = _act(x), x.device
     B, _ = _dims(x, "x", 2)
+    _need_all(state, "state")
     with _On(x, stream) as s:
-        _need_all(state, "state")
-        D, W, ldx = _conv_args(x, w, bias, state, None, (B,))
+        D, W, args = _conv_args(x, w, bias, state, None, (B,))
         if y is None:
             y = torch.empty((B, D), dtype=dt, device=dev)
-        _need(y, "y", dt, (B, D), dev)
-        st = _native.lib().kla_conv_step(
-            _ptr(x), ldx, _ptr(w), _ptr(bias), _ptr(state), _ptr(y), B, D, W, bool(silu),
-            _DT[dt], s)
+        st = _native.lib().kla_conv_step(*args[:5], _p(y, "y", dt, (B, D), dev), B, D, W,
+                                         bool(silu), _DT[dt], s)
     _check(st, "kla_conv_step")
     return y
 
@@ -782,25 +791,25 @@ def ssm_bwd_workspace_size(B: int, T: int, D: int, G: int, N: int) -> int:
 
 
 def _ssm_args(u, dt, A, Bm, Cm, D, z, dt_bias, lead):
-    """Checks the inputs that prompts and single tokens share; returns the
-    sizes and the row pitches of u, dt, Bm, Cm and z."""
+    """Sizes, the row pitches of u, dt, Bm, Cm and z, and the addresses of u ..
+    dt_bias, for prompts and single tokens."""
     ty, dev = u.dtype, u.device
     Dn = u.shape[-1]
-    _need_all(A, "A")
-    _need(A, "A", torch.float32, dev=dev)
-    if A.dim() != 2 or A.shape[0] != Dn:
-        raise ValueError("A must be [D, N] with D = %d, got %s" % (Dn, tuple(A.shape)))
+    if not isinstance(A, torch.Tensor) or A.dim() != 2 or A.shape[0] != Dn:
+        raise ValueError("A must be a [D, N] CUDA tensor with D = %d" % Dn)
     N = A.shape[1]
-    _need_all(Bm, "Bm")
     if not isinstance(Bm, torch.Tensor) or Bm.dim() != len(lead) + 2:
         raise ValueError("Bm must be a CUDA tensor of shape [..., G, N]")
     G = Bm.shape[-2]
-    _need(D, "D", torch.float32, (Dn,), dev)
-    _need(dt_bias, "dt_bias", torch.float32, (Dn,), dev)
-    lds = (_rows(u, "u", ty, lead, (Dn,), dev), _rows(dt, "dt", ty, lead, (Dn,), dev),
-           _rows(Bm, "Bm", ty, lead, (G, N), dev), _rows(Cm, "Cm", ty, lead, (G, N), dev),
-           0 if z is None else _rows(z, "z", ty, lead, (Dn,), dev))
-    return Dn, G, N, lds
+    ch, gn = (Dn,), (G, N)
+    lds = (_rows(u, "u", ty, lead, ch, dev), _rows(dt, "dt", ty, lead, ch, dev),
+           _rows(Bm, "Bm", ty, lead, gn, dev), _rows(Cm, "Cm", ty, lead, gn, dev),
+           0 if z is None else _rows(z, "z", ty, lead, ch, dev))
+    f32 = torch.float32
+    return Dn, G, N, lds, (
+        u.data_ptr(), dt.data_ptr(), _p(A, "A", f32, (Dn, N), dev), Bm.data_ptr(),
+        Cm.data_ptr(), _p(D, "D", f32, ch, dev), None if z is None else z.data_ptr(),
+        _p(dt_bias, "dt_bias", f32, ch, dev))
 
 
 def ssm_fwd(u, dt, A, Bm, Cm, D=None, z=None, dt_bias=None, h0=None, *, softplus: bool = True,
@@ -810,23 +819,20 @@ def ssm_fwd(u, dt, A, Bm, Cm, D=None, z=None, dt_bias=None, h0=None, *, softplus
     [B,T,D], Bm, Cm [B,T,G,N] bf16 or fp32 (rows may be parts of wider
     matrices), A [D,N], D, dt_bias [D], h0 [B,D,N] fp32, lengths [B] int32;
     N in {8, 16, 32, 64}.  Returns (y, hT)."""
-    ty, dev = _act(u, "u"), u.device
+    ty, dev, f32 = _act(u, "u"), u.device, torch.float32
     B, T, _ = _dims(u, "u", 3)
     with _On(u, stream) as s:
-        Dn, G, N, lds = _ssm_args(u, dt, A, Bm, Cm, D, z, dt_bias, (B, T))
-        _need(h0, "h0", torch.float32, (B, Dn, N), dev)
-        _need(lengths, "lengths", torch.int32, (B,), dev)
+        Dn, G, N, lds, args = _ssm_args(u, dt, A, Bm, Cm, D, z, dt_bias, (B, T))
         if y is None:
             y = torch.empty((B, T, Dn), dtype=ty, device=dev)
-        _need(y, "y", ty, (B, T, Dn), dev)
         if hT is None and return_state:
-            hT = torch.empty((B, Dn, N), dtype=torch.float32, device=dev)
-        _need(hT, "hT", torch.float32, (B, Dn, N), dev)
+            hT = torch.empty((B, Dn, N), dtype=f32, device=dev)
         workspace, nws = _scratch(workspace, ssm_fwd_workspace_size(B, T, Dn, G, N), dev)
         st = _native.lib().kla_ssm_fwd(
-            _ptr(u), _ptr(dt), _ptr(A), _ptr(Bm), _ptr(Cm), _ptr(D), _ptr(z), _ptr(dt_bias),
-            _ptr(h0), _ptr(lengths), _ptr(y), _ptr(hT), B, T, Dn, G, N, *lds, bool(softplus),
-            _DT[ty], _ptr(workspace), nws, s)
+            *args, _p(h0, "h0", f32, (B, Dn, N), dev),
+            _p(lengths, "lengths", torch.int32, (B,), dev), _p(y, "y", ty, (B, T, Dn), dev),
+            _p(hT, "hT", f32, (B, Dn, N), dev), B, T, Dn, G, N, *lds, bool(softplus), _DT[ty],
+            _ptr(workspace), nws, s)
     _check(st, "kla_ssm_fwd")
     return y, hT
 
@@ -840,13 +846,13 @@ def ssm_bwd(u, dt, A, Bm, Cm, grad_y, D=None, z=None, dt_bias=None, h0=None, gra
     need_h0)."""
     ty, dev = _act(u, "u"), u.device
     B, T, _ = _dims(u, "u", 3)
+    _need_all(grad_y, "grad_y")
     with _On(u, stream) as s:
-        Dn, G, N, lds = _ssm_args(u, dt, A, Bm, Cm, D, z, dt_bias, (B, T))
-        _need(h0, "h0", torch.float32, (B, Dn, N), dev)
-        _need(lengths, "lengths", torch.int32, (B,), dev)
-        _need_all(grad_y, "grad_y")
-        _need(grad_y, "grad_y", ty, (B, T, Dn), dev)
-        _need(grad_hT, "grad_hT", torch.float32, (B, Dn, N), dev)
+        Dn, G, N, lds, args = _ssm_args(u, dt, A, Bm, Cm, D, z, dt_bias, (B, T))
+        more = (_p(h0, "h0", torch.float32, (B, Dn, N), dev),
+                _p(lengths, "lengths", torch.int32, (B,), dev),
+                _p(grad_y, "grad_y", ty, (B, T, Dn), dev),
+                _p(grad_hT, "grad_hT", torch.float32, (B, Dn, N), dev))
         act = dict(dtype=ty, device=dev)
         f32 = dict(dtype=torch.float32, device=dev)
         out = dict(du=torch.empty((B, T, Dn), **act), ddt=torch.empty((B, T, Dn), **act),
@@ -858,11 +864,9 @@ def ssm_bwd(u, dt, A, Bm, Cm, grad_y, D=None, z=None, dt_bias=None, h0=None, gra
                    dh0=torch.empty((B, Dn, N), **f32) if need_h0 else None)
         workspace, nws = _scratch(workspace, ssm_bwd_workspace_size(B, T, Dn, G, N), dev)
         st = _native.lib().kla_ssm_bwd(
-            _ptr(u), _ptr(dt), _ptr(A), _ptr(Bm), _ptr(Cm), _ptr(D), _ptr(z), _ptr(dt_bias),
-            _ptr(h0), _ptr(lengths), _ptr(grad_y), _ptr(grad_hT), _ptr(out["du"]),
-            _ptr(out["ddt"]), _ptr(out["dA"]), _ptr(out["dB"]), _ptr(out["dC"]),
-            _ptr(out["dD"]), _ptr(out["dz"]), _ptr(out["ddt_bias"]), _ptr(out["dh0"]), B, T, Dn,
-            G, N, *lds, bool(softplus), _DT[ty], _ptr(workspace), nws, s)
+            *args, *more, *(_ptr(out[k]) for k in ("du", "ddt", "dA", "dB", "dC", "dD", "dz",
+                                                   "ddt_bias", "dh0")),
+            B, T, Dn, G, N, *lds, bool(softplus), _DT[ty], _ptr(workspace), nws, s)
     _check(st, "kla_ssm_bwd")
     return out
 
@@ -874,16 +878,14 @@ def ssm_step(u, dt, A, Bm, Cm, state, D=None, z=None, dt_bias=None, *, softplus:
     place.  Returns y [B,D]."""
     ty, dev = _act(u, "u"), u.device
     B, _ = _dims(u, "u", 2)
+    _need_all(state, "state")
     with _On(u, stream) as s:
-        Dn, G, N, lds = _ssm_args(u, dt, A, Bm, Cm, D, z, dt_bias, (B,))
-        _need_all(state, "state")
-        _need(state, "state", torch.float32, (B, Dn, N), dev)
+        Dn, G, N, lds, args = _ssm_args(u, dt, A, Bm, Cm, D, z, dt_bias, (B,))
         if y is None:
             y = torch.empty((B, Dn), dtype=ty, device=dev)
-        _need(y, "y", ty, (B, Dn), dev)
         st = _native.lib().kla_ssm_step(
-            _ptr(u), _ptr(dt), _ptr(A), _ptr(Bm), _ptr(Cm), _ptr(D), _ptr(z), _ptr(dt_bias),
-            _ptr(state), _ptr(y), B, Dn, G, N, *lds, bool(softplus), _DT[ty], s)
+            *args, _p(state, "state", torch.float32, (B, Dn, N), dev),
+            _p(y, "y", ty, (B, Dn), dev), B, Dn, G, N, *lds, bool(softplus), _DT[ty], s)
     _check(st, "kla_ssm_step")
     return y
 
@@ -892,31 +894,34 @@ _NORMS = {None: 0, "l2": 1, "rms": 2}
 
 
 def _qk_args(q, k, wq, wk, positions, inv_freq, norm):
+    """Sizes (B, T, Hq, Hk, d, rot), and the arguments q .. rot of the C calls
+    but for pos0, in two parts around it."""
     ty, dev = q.dtype, q.device
     one = q.dim() == 3  # a single token of each sequence: [B, H, d]
-    lead = (q.shape[0],) if one else tuple(q.shape[:2])
     if q.dim() not in (3, 4) or not isinstance(k, torch.Tensor) or k.dim() != q.dim():
         raise ValueError("q and k must be CUDA tensors [B, T, H, d] or [B, H, d]")
+    shape = tuple(q.shape)
+    lead, (Hq, d), Hk = shape[:-2], shape[-2:], k.shape[-2]
     B, T = lead[0], 1 if one else lead[1]
-    Hq, d = q.shape[-2:]
-    Hk = k.shape[-2]
     ldq, ldk = _rows(q, "q", ty, lead, (Hq, d), dev), _rows(k, "k", ty, lead, (Hk, d), dev)
-    _need(wq, "wq", torch.float32, (d,), dev)
-    _need(wk, "wk", torch.float32, (d,), dev)
-    _need(inv_freq, "inv_freq", torch.float32, dev=dev)
     if norm not in _NORMS:
         raise ValueError("norm must be None, 'l2' or 'rms', got %r" % (norm,))
-    stride = 0
+    stride = rot = 0
     if positions is not None:
-        _need(positions, "positions", torch.int32, dev=dev)
-        shape = tuple(positions.shape)
-        if shape == (lead if one else (B, T)):
+        have = tuple(positions.shape)
+        if have == lead:
             stride = T
-        elif one or shape != (T,):
+        elif one or have != (T,):
             raise ValueError("positions must have shape %s, got %s"
-                             % (lead if one else "%s or %s" % ((B, T), (T,)), shape))
-    rot = 0 if inv_freq is None else 2 * inv_freq.numel()
-    return B, T, Hq, Hk, d, ldq, ldk, stride, rot
+                             % (lead if one else "%s or %s" % (lead, (T,)), have))
+        _p(positions, "positions", torch.int32, have, dev)
+    if inv_freq is not None:
+        rot = 2 * inv_freq.numel()
+        _p(inv_freq, "inv_freq", torch.float32, inv_freq.shape, dev)
+    f32 = torch.float32
+    return (B, T, Hq, Hk, d, rot), (
+        q.data_ptr(), k.data_ptr(), ldq, ldk, _p(wq, "wq", f32, (d,), dev),
+        _p(wk, "wk", f32, (d,), dev), _ptr(positions), stride), (_ptr(inv_freq), rot)
 
 
 def qk_norm_bwd_workspace_size(B: int, T: int, Hq: int, Hk: int, d: int, rot: int) -> int:
@@ -933,17 +938,15 @@ def qk_norm_fwd(q, k, *, wq=None, wk=None, positions=None, inv_freq=None, pos0: 
     None = pos0 + t; inv_freq fp32, None = no rotation.  Returns (oq, ok)."""
     ty, dev = _act(q, "q"), q.device
     with _On(q, stream) as s:
-        B, T, Hq, Hk, d, ldq, ldk, ps, rot = _qk_args(q, k, wq, wk, positions, inv_freq, norm)
+        (B, T, Hq, Hk, d, _), head, freq = _qk_args(q, k, wq, wk, positions, inv_freq, norm)
         if oq is None:
             oq = torch.empty(q.shape, dtype=ty, device=dev)
         if ok is None:
             ok = torch.empty(k.shape, dtype=ty, device=dev)
-        _need(oq, "oq", ty, q.shape, dev)
-        _need(ok, "ok", ty, k.shape, dev)
         st = _native.lib().kla_qk_norm_fwd(
-            _ptr(q), _ptr(k), ldq, ldk, _ptr(wq), _ptr(wk), _ptr(positions), ps, pos0,
-            _ptr(inv_freq), rot, bool(interleaved), float(scale), _NORMS[norm], float(eps),
-            _ptr(oq), _ptr(ok), B, T, Hq, Hk, d, _DT[ty], s)
+            *head, pos0, *freq, bool(interleaved), scale, _NORMS[norm], eps,
+            _p(oq, "oq", ty, q.shape, dev), _p(ok, "ok", ty, k.shape, dev), B, T, Hq, Hk, d,
+            _DT[ty], s)
     _check(st, "kla_qk_norm_fwd")
     return oq, ok
 
@@ -955,11 +958,11 @@ def qk_norm_bwd(q, k, grad_oq, grad_ok, *, wq=None, wk=None, positions=None, inv
     q's type, dwq, dwk fp32 (None for weights that are None)."""
     ty, dev = _act(q, "q"), q.device
     with _On(q, stream) as s:
-        B, T, Hq, Hk, d, ldq, ldk, ps, rot = _qk_args(q, k, wq, wk, positions, inv_freq, norm)
+        (B, T, Hq, Hk, d, rot), head, freq = _qk_args(q, k, wq, wk, positions, inv_freq, norm)
         _need_all(grad_oq, "grad_oq")
         _need_all(grad_ok, "grad_ok")
-        _need(grad_oq, "grad_oq", ty, q.shape, dev)
-        _need(grad_ok, "grad_ok", ty, k.shape, dev)
+        gq, gk = _p(grad_oq, "grad_oq", ty, q.shape, dev), _p(grad_ok, "grad_ok", ty, k.shape,
+                                                              dev)
         out = dict(dq=torch.empty(q.shape, dtype=ty, device=dev),
                    dk=torch.empty(k.shape, dtype=ty, device=dev),
                    dwq=None if wq is None else torch.empty_like(wq),
@@ -969,10 +972,8 @@ def qk_norm_bwd(q, k, grad_oq, grad_ok, *, wq=None, wk=None, positions=None, inv
             need = qk_norm_bwd_workspace_size(B, T, Hq, Hk, d, rot)
         workspace, nws = _scratch(workspace, need, dev)
         st = _native.lib().kla_qk_norm_bwd(
-            _ptr(q), _ptr(k), ldq, ldk, _ptr(wq), _ptr(wk), _ptr(positions), ps, pos0,
-            _ptr(inv_freq), rot, bool(interleaved), float(scale), _NORMS[norm], float(eps),
-            _ptr(grad_oq), _ptr(grad_ok), _ptr(out["dq"]), _ptr(out["dk"]), _ptr(out["dwq"]),
-            _ptr(out["dwk"]), B, T, Hq, Hk, d, _DT[ty], _ptr(workspace), nws, s)
+            *head, pos0, *freq, bool(interleaved), scale, _NORMS[norm], eps, gq, gk,
+            _ptr(out["dq"]), _ptr(out["dk"]), _ptr(out["dwq"]), _ptr(out["dwk"]), B, T, Hq, Hk, d, _DT[ty], _ptr(workspace), nws, s)
     _check(st, "kla_qk_norm_bwd")
     return out
 
