@@ -691,8 +691,9 @@ def _scratch(workspace, need, dev):
 
 
 def _dims(t, name, n):
-    if t.dim() != n:
-        raise ValueError("%s must have %d dimensions, got %s" % (name, n, tuple(t.shape)))
+    if t.dim() != n or max(t.shape) >= 1 << 31:
+        raise ValueError("%s must have %d dimensions below 2^31, got %s"
+                         % (name, n, tuple(t.shape)))
     return tuple(t.shape)
 
 
@@ -893,7 +894,7 @@ def ssm_step(u, dt, A, Bm, Cm, state, D=None, z=None, dt_bias=None, *, softplus:
 _NORMS = {None: 0, "l2": 1, "rms": 2}
 
 
-def _qk_args(q, k, wq, wk, positions, inv_freq, norm):
+def _qk_args(q, k, wq, wk, positions, inv_freq, norm, pos0):
     """Sizes (B, T, Hq, Hk, d, rot), and the arguments q .. rot of the C calls
     but for pos0, in two parts around it."""
     ty, dev = q.dtype, q.device
@@ -901,6 +902,8 @@ def _qk_args(q, k, wq, wk, positions, inv_freq, norm):
     if q.dim() not in (3, 4) or not isinstance(k, torch.Tensor) or k.dim() != q.dim():
         raise ValueError("q and k must be CUDA tensors [B, T, H, d] or [B, H, d]")
     shape = tuple(q.shape)
+    if max(shape) >= 1 << 31:
+        raise ValueError("q must have dimensions below 2^31, got %s" % (shape,))
     lead, (Hq, d), Hk = shape[:-2], shape[-2:], k.shape[-2]
     B, T = lead[0], 1 if one else lead[1]
     ldq, ldk = _rows(q, "q", ty, lead, (Hq, d), dev), _rows(k, "k", ty, lead, (Hk, d), dev)
@@ -915,6 +918,8 @@ def _qk_args(q, k, wq, wk, positions, inv_freq, norm):
             raise ValueError("positions must have shape %s, got %s"
                              % (lead if one else "%s or %s" % (lead, (T,)), have))
         _p(positions, "positions", torch.int32, have, dev)
+    elif not -(1 << 31) <= pos0 <= (1 << 31) - max(T, 1):
+        raise ValueError("positions from pos0 = %d on pass 32 bits" % pos0)
     if inv_freq is not None:
         rot = 2 * inv_freq.numel()
         _p(inv_freq, "inv_freq", torch.float32, inv_freq.shape, dev)
@@ -938,7 +943,8 @@ def qk_norm_fwd(q, k, *, wq=None, wk=None, positions=None, inv_freq=None, pos0: 
     None = pos0 + t; inv_freq fp32, None = no rotation.  Returns (oq, ok)."""
     ty, dev = _act(q, "q"), q.device
     with _On(q, stream) as s:
-        (B, T, Hq, Hk, d, _), head, freq = _qk_args(q, k, wq, wk, positions, inv_freq, norm)
+        (B, T, Hq, Hk, d, _), head, freq = _qk_args(q, k, wq, wk, positions, inv_freq, norm,
+                                                     pos0)
         if oq is None:
             oq = torch.empty(q.shape, dtype=ty, device=dev)
         if ok is None:
@@ -958,7 +964,8 @@ def qk_norm_bwd(q, k, grad_oq, grad_ok, *, wq=None, wk=None, positions=None, inv
     q's type, dwq, dwk fp32 (None for weights that are None)."""
     ty, dev = _act(q, "q"), q.device
     with _On(q, stream) as s:
-        (B, T, Hq, Hk, d, rot), head, freq = _qk_args(q, k, wq, wk, positions, inv_freq, norm)
+        (B, T, Hq, Hk, d, rot), head, freq = _qk_args(q, k, wq, wk, positions, inv_freq, norm,
+                                                     pos0)
         _need_all(grad_oq, "grad_oq")
         _need_all(grad_ok, "grad_ok")
         gq, gk = _p(grad_oq, "grad_oq", ty, q.shape, dev), _p(grad_ok, "grad_ok", ty, k.shape,

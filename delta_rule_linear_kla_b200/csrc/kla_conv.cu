@@ -569,8 +569,8 @@ kla_status kla_conv_fwd(const void* x, long long ldx, const float* w, const floa
   kla_status s = check(B, T, D, W, dtype, ldx);
   if (s != KLA_OK) return s;
   if (T > 0 && (!x || !w || !y)) return KLA_ERR_INVALID_ARG;
-  const void* const ptrs[] = {w, bias, s0, lengths, y, sT};
-  if (misaligned(ptrs) || misplaced(x, elem(dtype))) return KLA_ERR_INVALID_ARG;
+  const void* const ptrs[] = {w, bias, s0, y, sT};
+  if (misaligned(ptrs) || misplaced(lengths, 4) || misplaced(x, elem(dtype))) return KLA_ERR_INVALID_ARG;
   const int es = elem(dtype);
   const long long rows = (long long)B * T, ns = (long long)B * (W - 1) * D;
   const Span in[] = {span(x, rows, D, ldx, es), span(w, (long long)D * W, 4),
@@ -614,9 +614,9 @@ kla_status kla_conv_bwd(const void* x, long long ldx, const float* w, const floa
   if (s != KLA_OK) return s;
   if (T > 0 && (!x || !grad_y || !grad_x)) return KLA_ERR_INVALID_ARG;
   if (!w || !grad_w) return KLA_ERR_INVALID_ARG;
-  const void* const ptrs[] = {w,      bias,   s0,        lengths, grad_y,   grad_sT,
+  const void* const ptrs[] = {w,      bias,   s0,        grad_y,  grad_sT,
                               grad_x, grad_w, grad_bias, grad_s0, workspace};
-  if (misaligned(ptrs) || misplaced(x, elem(dtype))) return KLA_ERR_INVALID_ARG;
+  if (misaligned(ptrs) || misplaced(lengths, 4) || misplaced(x, elem(dtype))) return KLA_ERR_INVALID_ARG;
   const size_t need = kla_conv_bwd_workspace_size(B, T, D, W);
   if (ws_bytes < need || (need && !workspace)) return KLA_ERR_INVALID_ARG;
   const int es = elem(dtype);

@@ -457,6 +457,12 @@ static kla_status check(int B, int T, int Hq, int Hk, int d, int rot, int norm, 
   return KLA_OK;
 }
 
+// Read one by one, these need only their own alignment.
+static bool scalars_misplaced(const float* wq, const float* wk, const int* pos,
+                              const float* inv_freq) {
+  return misplaced(wq, 4) || misplaced(wk, 4) || misplaced(pos, 4) || misplaced(inv_freq, 4);
+}
+
 static long long parts_of(long long tokens, int H, int d) {
   return tokens == 0 ? 0 : blocks_of(tokens, tokens_per_block(H, d, tokens), true);
 }
@@ -478,11 +484,12 @@ kla_status kla_qk_norm_fwd(const void* q, const void* k, long long ldq, long lon
   kla_status s = check(B, T, Hq, Hk, d, rot, norm, eps, scale, ldq, ldk, dtype);
   if (s != KLA_OK) return s;
   if (T == 0) return KLA_OK;
+  if (!positions && (long long)pos0 + T - 1 > 0x7fffffffLL) return KLA_ERR_INVALID_ARG;
   if ((Hq && (!q || !oq)) || (Hk && (!k || !ok)) || (rot && !inv_freq) ||
       (positions && pos_stride != 0 && pos_stride < T))
     return KLA_ERR_INVALID_ARG;
-  const void* const ptrs[] = {q, k, wq, wk, positions, inv_freq, oq, ok};
-  if (misaligned(ptrs)) return KLA_ERR_INVALID_ARG;
+  const void* const ptrs[] = {q, k, oq, ok};
+  if (misaligned(ptrs) || scalars_misplaced(wq, wk, positions, inv_freq)) return KLA_ERR_INVALID_ARG;
   const int es = elem(dtype);
   const long long rows = (long long)B * T, nq = (long long)Hq * d, nk = (long long)Hk * d;
   const Span in[] = {span(q, rows, nq, ldq, es), span(k, rows, nk, ldk, es),
@@ -519,10 +526,11 @@ kla_status kla_qk_norm_bwd(const void* q, const void* k, long long ldq, long lon
                            void* stream) {
   kla_status s = check(B, T, Hq, Hk, d, rot, norm, eps, scale, ldq, ldk, dtype);
   if (s != KLA_OK) return s;
+  if (!positions && (long long)pos0 + T - 1 > 0x7fffffffLL) return KLA_ERR_INVALID_ARG;
   const bool weights = grad_wq || grad_wk;
-  const void* const ptrs[] = {q, k, wq, wk, positions, inv_freq, grad_oq, grad_ok,
-                              grad_q, grad_k, grad_wq, grad_wk, workspace};
-  if (misaligned(ptrs)) return KLA_ERR_INVALID_ARG;
+  const void* const ptrs[] = {q,      k,      grad_oq, grad_ok,  grad_q,
+                              grad_k, grad_wq, grad_wk, workspace};
+  if (misaligned(ptrs) || scalars_misplaced(wq, wk, positions, inv_freq)) return KLA_ERR_INVALID_ARG;
   cudaStream_t st = (cudaStream_t)stream;
   cudaError_t e = cudaSuccess;
   const size_t need = weights ? kla_qk_norm_bwd_workspace_size(B, T, Hq, Hk, d, rot) : 0;

@@ -796,11 +796,13 @@ bwd_kernel(BwdArgs q) {
   // sums of dt'
   float4* const s_h = reinterpret_cast<float4*>(smem + 2 * Sh::BUF) + tid;
   float2* const s_s = reinterpret_cast<float2*>(s_h - tid + 8 * CW * 32) + tid;
-  if (cc + 1 >= nc) {  // channels that do not exist are never copied
 #pragma unroll
-    for (int i = 0; i < 8; ++i) s_h[i * CW * 32] = make_float4(0.f, 0.f, 0.f, 0.f);
-    s_s[0] = s_s[CW * 32] = make_float2(0.f, 0.f);
-  }
+  for (int c = 0; c < 2; ++c)
+    if (cc + c >= nc) {  // a channel that does not exist is never copied
+#pragma unroll
+      for (int i = 0; i < 8; i += 2) s_h[(i + c) * CW * 32] = make_float4(0.f, 0.f, 0.f, 0.f);
+      reinterpret_cast<float*>(s_s)[c] = reinterpret_cast<float*>(s_s + CW * 32)[c] = 0.f;
+    }
   auto fetch = [&](int k) {
     const int t = t_lo + k * K;
     const long long ck = (long long)b * nck + t / K;
@@ -1349,8 +1351,8 @@ kla_status kla_ssm_fwd(const void* u, const void* dt, const float* A, const void
                        size_t ws_bytes, void* stream) {
   kla_status s = check(B, T, D, G, N, dtype);
   if (s != KLA_OK) return s;
-  const void* const ptrs[] = {A, Dw, dt_bias, h0, lengths, y, hT, workspace};
-  if (misaligned(ptrs) || rows_misplaced(u, dt, Bm, Cm, z, elem(dtype))) return KLA_ERR_INVALID_ARG;
+  const void* const ptrs[] = {A, Dw, dt_bias, h0, y, hT, workspace};
+  if (misaligned(ptrs) || misplaced(lengths, 4) || rows_misplaced(u, dt, Bm, Cm, z, elem(dtype))) return KLA_ERR_INVALID_ARG;
   const long long rows = (long long)B * T, dn = (long long)D * N, ns = B * dn;
   cudaStream_t st = (cudaStream_t)stream;
   cudaError_t e = cudaSuccess;
@@ -1411,10 +1413,9 @@ kla_status kla_ssm_bwd(const void* u, const void* dt, const float* A, const void
                        void* stream) {
   kla_status s = check(B, T, D, G, N, dtype);
   if (s != KLA_OK) return s;
-  const void* const ptrs[] = {A, Dw, dt_bias, h0, lengths, grad_y, grad_hT, grad_u, grad_dt,
-                              grad_A, grad_B, grad_C, grad_D, grad_z, grad_dt_bias, grad_h0,
-                              workspace};
-  if (misaligned(ptrs) || rows_misplaced(u, dt, Bm, Cm, z, elem(dtype))) return KLA_ERR_INVALID_ARG;
+  const void* const ptrs[] = {A, Dw, dt_bias, h0, grad_y, grad_hT, grad_u, grad_dt, grad_A,
+                              grad_B, grad_C, grad_D, grad_z, grad_dt_bias, grad_h0, workspace};
+  if (misaligned(ptrs) || misplaced(lengths, 4) || rows_misplaced(u, dt, Bm, Cm, z, elem(dtype))) return KLA_ERR_INVALID_ARG;
   if (!grad_A || (z && T > 0 && !grad_z)) return KLA_ERR_INVALID_ARG;
   const long long rows = (long long)B * T, dn = (long long)D * N, ns = B * dn;
   if (T > 0) {

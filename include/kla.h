@@ -422,7 +422,8 @@ KLA_API kla_status kla_gdn_recurrent_bwd(const void *q, const void *k, const voi
  *   * Inputs marked [ld] may be rows of a wider matrix (a projection's
  *     output): row r (token b * T + t) starts ld elements after row r - 1, and
  *     its elements are contiguous.  ld is at least the row's length.  They
- *     need only their element's alignment (q and k of the norm: 16 bytes).
+ *     need only their element's alignment (q and k of the norm: 16 bytes), and
+ *     so do lengths, positions, inv_freq and the norm's weights.
  *   * Gradients of activations have the activations' type, gradients of
  *     parameters and of fp32 states are fp32.
  *   * lengths ([B] int32 on the device, nullable): sequence b has
@@ -531,7 +532,7 @@ KLA_API kla_status kla_ssm_step(const void *u, const void *dt, const float *A, c
  *   q [B][T][Hq][d] dtype [ldq], k [B][T][Hk][d] dtype [ldk] (Hq or Hk may be 0)
  *   wq, wk [d] fp32, nullable = 1;  inv_freq [rot/2] fp32 (rot = 0: none)
  *   positions: int32 [B][T] with rows pos_stride apart (0: one row for all
- *   sequences); NULL = pos0 + t.  Angles are formed in fp64.
+ *   sequences); NULL = pos0 + t, at most 2^31 - 1.  Angles are formed in fp64.
  *   oq, ok: contiguous, dtype, written.
  * d a multiple of 8, at most 256; ldq and ldk multiples of 16 bytes (else
  * KLA_ERR_UNSUPPORTED); rot even, at most d.  Inverse frequencies stretched

@@ -201,6 +201,7 @@ def test_qk_norm_refusals(lib):
     assert fwd(ldq=255) == fwd(rot=130) == fwd(rot=63) == fwd(norm=3) == fwd(eps=-1.0) == INVALID
     assert fwd(eps=float("nan")) == fwd(scale=float("inf")) == fwd(Hq=0, Hk=0) == INVALID
     assert fwd(pos=4 * A, ps=7) == INVALID           # rows of positions overlap
+    assert fwd(pos=4 * A + 2, ps=8) == fwd(f=3 * A + 1) == fwd(q=A + 8) == INVALID  # misaligned
     assert fwd(d=100, ldq=200, ldk=104, rot=0) == UNSUPPORTED
     assert fwd(d=264, ldq=528, ldk=264) == UNSUPPORTED
     assert fwd(ldq=260) == UNSUPPORTED               # rows not 16-byte multiples apart

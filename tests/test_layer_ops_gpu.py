@@ -79,6 +79,7 @@ CONV = [  # B, T, D, W, dtype, silu, bias, state, lengths, wide
     (3, 130, 33, 2, "fp32", False, True, True, [130, 64, 0], False),
     (1, 1037, 24, 4, "bf16", True, True, True, None, False),
     (2, 260, 100, 4, "bf16", True, True, True, [-3, 999], False),  # clamped to 0 and T
+    (1, 9, 257, 4, "bf16", True, True, True, None, True),  # odd rows of a wide matrix
 ]
 
 
@@ -155,6 +156,10 @@ SSM = [  # B, T, D, G, N, dtype, z, skip, bias, softplus, state, lengths, wide
     (1, 95, 66, 1, 64, "fp32", True, False, True, True, True, None, True),
     (2, 100, 200, 1, 16, "fp32", True, True, True, True, True, [100, 49], False),
     (1, 130, 300, 2, 8, "bf16", True, True, False, True, True, None, True),
+    (2, 8, 129, 1, 16, "bf16", True, True, True, True, True, None, False),  # 2 tiles and 1
+    (2, 9, 65, 1, 8, "bf16", True, True, True, True, True, [9, 8], False),
+    (1, 40, 6, 6, 16, "fp32", False, True, True, True, True, None, False),  # groups of one
+    (1, 41, 33, 1, 32, "bf16", True, True, True, True, True, None, True),
     (1, 1300, 10, 1, 16, "fp32", True, True, True, True, True, None, False),   # segments
     (2, 1100, 6, 2, 8, "bf16", True, True, True, True, True, [1100, 700], False),
 ]
@@ -328,9 +333,18 @@ def test_qk_norm_positions():
     b = api.qk_norm_fwd(q, k, inv_freq=f, positions=pos)
     c = api.qk_norm_fwd(q, k, inv_freq=f, positions=pos.expand(2, 9).contiguous())
     one = api.qk_norm_fwd(q[:, 3], k[:, 3], inv_freq=f, positions=pos[3:4].expand(2).contiguous())
+    part = api.qk_norm_fwd(q[:, 2:5].contiguous(), k[:, 2:5].contiguous(), inv_freq=f,
+                           positions=pos[2:5])  # not 16-byte aligned
     for i in range(2):
         assert torch.equal(a[i], b[i]) and torch.equal(a[i], c[i])
-        assert torch.equal(one[i], a[i][:, 3])
+        assert torch.equal(one[i], a[i][:, 3]) and torch.equal(part[i], a[i][:, 2:5])
+    with pytest.raises(ValueError, match="32 bits"):
+        api.qk_norm_fwd(q, k, inv_freq=f, pos0=2**31 - 4)
+    a = api.qk_norm_fwd(q, k, inv_freq=f, pos0=2**31 - 9)
+    pos = (2**31 - 9 + torch.arange(9)).expand(2, 9)
+    # the fp64 product of a 31-bit position and a 24-bit frequency is off by
+    # 2^-53 of up to 2^31 radians, 2^-22: 4 units beside the c = 64
+    check(a[0], ref.head_norm(q, None, pos, f), 68)
 
 
 # ------------------------------------------------ gradients through autograd
