@@ -207,13 +207,11 @@ scan_kernel(Args p) {
 #pragma unroll
       for (int i = 0; i < IX; ++i) {
         const int tt = tt0 + i * TS;
-        float4 d = dn[i].get(), x = xn[i].get();
-        d.x += bias.x; d.y += bias.y; d.z += bias.z; d.w += bias.w;
-        if (sp) {
-          d.x = softplus(d.x); d.y = softplus(d.y); d.z = softplus(d.z); d.w = softplus(d.w);
-        }
+        Quad d4 = quad(dn[i].get()) + quad(bias), x4 = quad(xn[i].get());
+        if (sp) d4 = softplus4(d4);
         // tokens that do not exist, and channels past the last, step by 0:
         // their state stays as it is
+        float4 d = flat(d4);
         if (ends) {
           const int n = t0 + tt < t_live ? m : 0;
           if (n < 1) d.x = 0.f;
@@ -221,14 +219,11 @@ scan_kernel(Args p) {
           if (n < 3) d.z = 0.f;
           if (n < 4) d.w = 0.f;
         }
-        if (REV) {
-          if (has_z) {
-            const float4 q = zn[i].get();
-            x.x *= silu(q.x); x.y *= silu(q.y); x.z *= silu(q.z); x.w *= silu(q.w);
-          }
-        } else {
-          x.x *= d.x; x.y *= d.y; x.z *= d.z; x.w *= d.w;
-        }
+        if (!REV)
+          x4 = x4 * quad(d);
+        else if (has_z)
+          x4 = x4 * silu4(quad(zn[i].get()));
+        const float4 x = flat(x4);
         *reinterpret_cast<float4*>(sd + tt * CH + c) = d;
         *reinterpret_cast<float4*>(sx + tt * CH + c) = x;
       }
@@ -248,15 +243,10 @@ scan_kernel(Args p) {
         T* py = y + (long long)(t0 + tt0) * p.D;
 #pragma unroll
         for (int i = 0; i < IX; ++i) {
-          const float4 q = xs[i].get();
-          float4 v = *reinterpret_cast<const float4*>(sy + (tt0 + i * TS) * CH + c);
-          v.x = fmaf(skip.x, q.x, v.x); v.y = fmaf(skip.y, q.y, v.y);
-          v.z = fmaf(skip.z, q.z, v.z); v.w = fmaf(skip.w, q.w, v.w);
-          if (has_z) {
-            const float4 w = zs[i].get();
-            v.x *= silu(w.x); v.y *= silu(w.y); v.z *= silu(w.z); v.w *= silu(w.w);
-          }
-          IO<T>::st4(py, v);
+          Quad v = quad(*reinterpret_cast<const float4*>(sy + (tt0 + i * TS) * CH + c));
+          v = fma4(quad(skip), quad(xs[i].get()), v);
+          if (has_z) v = v * silu4(quad(zs[i].get()));
+          IO<T>::st4(py, flat(v));
           py += (long long)TS * p.D;
         }
         return;
@@ -267,14 +257,10 @@ scan_kernel(Args p) {
         if (t >= t_hi || m <= 0) continue;
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
         if (t < t_live) {
-          const float4 q = xs[i].get();
-          v = *reinterpret_cast<const float4*>(sy + tt * CH + c);
-          v.x = fmaf(skip.x, q.x, v.x); v.y = fmaf(skip.y, q.y, v.y);
-          v.z = fmaf(skip.z, q.z, v.z); v.w = fmaf(skip.w, q.w, v.w);
-          if (has_z) {
-            const float4 w = zs[i].get();
-            v.x *= silu(w.x); v.y *= silu(w.y); v.z *= silu(w.z); v.w *= silu(w.w);
-          }
+          Quad w = quad(*reinterpret_cast<const float4*>(sy + tt * CH + c));
+          w = fma4(quad(skip), quad(xs[i].get()), w);
+          if (has_z) w = w * silu4(quad(zs[i].get()));
+          v = flat(w);
         }
         st4(y + (long long)t * p.D, v, m, vec);
       }
@@ -643,21 +629,16 @@ bwd_kernel(BwdArgs q) {
       for (int i = 0; i < IX; ++i) {
         const int tt = tt0 + i * TS;
         if (XG < NH && hid >= XG) continue;
-        float4 d = next.dt[i].get(), x = next.u[i].get(), gg = next.gy[i].get();
-        d.x += bias.x; d.y += bias.y; d.z += bias.z; d.w += bias.w;
-        if (sp) {
-          d.x = softplus(d.x); d.y = softplus(d.y); d.z = softplus(d.z); d.w = softplus(d.w);
-        }
+        Quad d4 = quad(next.dt[i].get()) + quad(bias), g4 = quad(next.gy[i].get());
+        if (sp) d4 = softplus4(d4);
+        float4 d = flat(d4);
         const int n = t0 + tt < t_live ? m : 0;  // zero steps as in the scan
         if (n < 1) d.x = 0.f;
         if (n < 2) d.y = 0.f;
         if (n < 3) d.z = 0.f;
         if (n < 4) d.w = 0.f;
-        if (has_z) {
-          const float4 w = next.z[i].get();
-          gg.x *= silu(w.x); gg.y *= silu(w.y); gg.z *= silu(w.z); gg.w *= silu(w.w);
-        }
-        x.x *= d.x; x.y *= d.y; x.z *= d.z; x.w *= d.w;
+        if (has_z) g4 = g4 * silu4(quad(next.z[i].get()));
+        const float4 x = flat(quad(next.u[i].get()) * quad(d)), gg = flat(g4);
         float* o = buf + tt * CH + c;
         *reinterpret_cast<float4*>(o) = d;
         *reinterpret_cast<float4*>(o + Sh::XS) = x;
@@ -686,35 +667,21 @@ bwd_kernel(BwdArgs q) {
         float4 vdu = make_float4(0.f, 0.f, 0.f, 0.f), vddt = vdu, vdz = vdu;
         if (t < t_live) {
           const float* o = buf + tt * CH + c;
-          const float4 d = *reinterpret_cast<const float4*>(o);
-          const float4 gg = *reinterpret_cast<const float4*>(o + 2 * Sh::XS);
-          const float4 sB = *reinterpret_cast<const float4*>(o + 3 * Sh::XS);
-          const float4 sA = *reinterpret_cast<const float4*>(o + 4 * Sh::XS);
-          const float4 y0 = *reinterpret_cast<const float4*>(o + 5 * Sh::XS);
-          const float4 uu = done.u[i].get(), raw = done.dt[i].get();
-          auto one = [&](float d, float gg, float sB, float sA, float uu, float raw, float skip,
-                         float& du, float& ddt, float& aD, float& aT) {
-            du = fmaf(skip, gg, sB * d);
-            // sA is the sum with A log2 e
-            ddt = fmaf(sB, uu, sA * 0.6931471805599453f);
-            if (sp) ddt *= sigmoid(raw);
-            aD = fmaf(gg, uu, aD);
-            aT += ddt;
+          auto at = [&](int j) {
+            return quad(*reinterpret_cast<const float4*>(o + j * Sh::XS));
           };
-          one(d.x, gg.x, sB.x, sA.x, uu.x, raw.x + bias.x, skip.x, vdu.x, vddt.x, accD.x, accT.x);
-          one(d.y, gg.y, sB.y, sA.y, uu.y, raw.y + bias.y, skip.y, vdu.y, vddt.y, accD.y, accT.y);
-          one(d.z, gg.z, sB.z, sA.z, uu.z, raw.z + bias.z, skip.z, vdu.z, vddt.z, accD.z, accT.z);
-          one(d.w, gg.w, sB.w, sA.w, uu.w, raw.w + bias.w, skip.w, vdu.w, vddt.w, accD.w, accT.w);
+          const Quad d = at(0), gg = at(2), sB = at(3), uu = quad(done.u[i].get());
+          vdu = flat(fma4(quad(skip), gg, sB * d));
+          // the sum over A h e is with A log2 e
+          Quad ds = fma4(sB, uu, at(4) * all4(0.6931471805599453f));
+          if (sp) ds = ds * sigmoid4(quad(done.dt[i].get()) + quad(bias));
+          vddt = flat(ds);
+          accD = flat(fma4(gg, uu, quad(accD)));
+          accT = flat(quad(accT) + ds);
           if (has_z) {
-            const float4 zz = done.z[i].get(), g0 = done.gy[i].get();
-            auto gate = [&](float z, float g0, float y0, float skip, float uu) {
-              const float s = sigmoid(z);
-              return g0 * fmaf(skip, uu, y0) * (s * fmaf(z, 1.f - s, 1.f));
-            };
-            vdz = make_float4(gate(zz.x, g0.x, y0.x, skip.x, uu.x),
-                              gate(zz.y, g0.y, y0.y, skip.y, uu.y),
-                              gate(zz.z, g0.z, y0.z, skip.z, uu.z),
-                              gate(zz.w, g0.w, y0.w, skip.w, uu.w));
+            const Quad zz = quad(done.z[i].get()), s = sigmoid4(zz), one = all4(1.f);
+            const Quad slope = s * fma4(zz, fma4(s, all4(-1.f), one), one);
+            vdz = flat(quad(done.gy[i].get()) * fma4(quad(skip), uu, at(5)) * slope);
           }
         }
         st4(du + (long long)t * p.D, vdu, m, vec);
