@@ -423,7 +423,7 @@ scan_kernel(Args p) {
 // that segment s starts from.  REV walks from the last segment to the first.
 template <bool REV>
 __global__ void __launch_bounds__(256)
-chain_kernel(const float* __restrict__ A, const float* __restrict__ h0, float* __restrict__ ends,
+chain_kernel(const float* __restrict__ A, const float* __restrict__ h0, float* ends,
              const float* __restrict__ sums, int S, int D, int N, long long total) {
   const long long id = (long long)blockIdx.x * 256 + threadIdx.x;
   if (id >= total) return;
@@ -432,16 +432,24 @@ chain_kernel(const float* __restrict__ A, const float* __restrict__ h0, float* _
   const int d = (int)(at / N);
   const float a2 = A[at] * kLog2e;
   float h = h0 ? h0[id] : 0.f;
-  for (int i = 0; i < S; ++i) {
-    const int s = REV ? S - 1 - i : i;
-    float* e = ends + (b * S + s) * dn + at;
-    if (i == S - 1) {
-      *e = h;
-      return;
+  // eight segments' values are loaded before the first is needed
+  for (int i0 = 0; i0 < S; i0 += 8) {
+    float own[8], sum[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int i = i0 + j, s = REV ? S - 1 - i : i;
+      own[j] = sum[j] = 0.f;
+      if (i < S - 1) {
+        own[j] = ends[(b * S + s) * dn + at];
+        sum[j] = sums[(b * S + s) * D + d];
+      }
     }
-    const float own = *e;
-    *e = h;
-    h = fmaf(ex2(a2 * sums[(b * S + s) * D + d]), h, own);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int i = i0 + j, s = REV ? S - 1 - i : i;
+      if (i < S) ends[(b * S + s) * dn + at] = h;
+      h = fmaf(ex2(a2 * sum[j]), h, own[j]);
+    }
   }
 }
 
