@@ -598,7 +598,10 @@ def kda_decode_step_beta(q, k, v, g, beta, S, *, o=None, stream=None):
 # Layer operators around the recurrences: short causal convolution, selective
 # state space scan, norm and rotation of queries and keys.
 
-# handle of a device's current stream, without the Stream object around it
+# The current device, and the handle of a device's current stream without the
+# Stream object around it.  (Both are asked for after a CUDA tensor was seen, so
+# CUDA is initialised.)
+_this_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 
@@ -613,9 +616,8 @@ class _On:
         self.dev, self.stream, self.ctx = ref.device, stream, None
 
     def __enter__(self):
-        if self.stream is None and torch.cuda.current_device() == self.dev.index:
+        if self.stream is None and _this_device() == self.dev.index:
             return _raw_stream(self.dev.index)
-        self.ctx = contextlib.ExitStack()
         with contextlib.ExitStack() as stack:
             stack.enter_context(torch.cuda.device(self.dev))
             s = torch.cuda.current_stream(self.dev) if self.stream is None else self.stream
@@ -630,12 +632,17 @@ class _On:
             self.ctx.close()
 
 
+def _like(t):
+    """A new contiguous tensor of t's shape and type."""
+    return torch.empty_like(t, memory_format=torch.contiguous_format)
+
+
 def _p(t, name, dtype, shape, dev):
     """Address of a contiguous argument (None stays None); _need's checks, and
     its words where one fails."""
     if t is None:
         return None
-    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.device == dev
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == dev.index
             and t.shape == shape and t.is_contiguous()):
         _need(t, name, dtype, shape, dev)
     return t.data_ptr()
@@ -644,34 +651,34 @@ def _p(t, name, dtype, shape, dev):
 def _rows(t, name, dtype, lead, inner, dev):
     """Elements between the rows of an input that may be rows of a wider
     matrix: shape lead + inner, inner contiguous, rows evenly spaced."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise ValueError("%s must be a CUDA tensor" % name)
-    if t.device != dev:
-        raise ValueError("%s is on %s, the call's other tensors on %s" % (name, t.device, dev))
-    if t.dtype is not dtype:
-        raise ValueError("%s must be %s, got %s" % (name, dtype, t.dtype))
     shape = lead + inner
-    if t.shape != shape:
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == dev.index
+            and t.shape == shape):
+        if not isinstance(t, torch.Tensor) or not t.is_cuda:
+            raise ValueError("%s must be a CUDA tensor" % name)
+        if t.device != dev:
+            raise ValueError("%s is on %s, the call's other tensors on %s"
+                             % (name, t.device, dev))
+        if t.dtype is not dtype:
+            raise ValueError("%s must be %s, got %s" % (name, dtype, t.dtype))
         raise ValueError("%s must have shape %s, got %s" % (name, shape, tuple(t.shape)))
     n = inner[0] if len(inner) == 1 else inner[0] * inner[1]
     if t.is_contiguous() or t.numel() == 0:
         return n
-    st, want = t.stride(), 1
-    for i in range(len(shape) - 1, len(lead) - 1, -1):
-        if st[i] != want and shape[i] != 1:
-            raise ValueError("%s: the elements of a row must be contiguous" % name)
-        want *= shape[i]
-    ld, span = None, 1
-    for i in range(len(lead) - 1, -1, -1):
-        if lead[i] != 1:
-            if ld is None:
-                ld = st[i]  # the rows before are single
-                if ld < n:
-                    raise ValueError("%s: rows must not overlap" % name)
-            if st[i] != ld * span:
-                raise ValueError("%s: rows must be evenly spaced" % name)
-            span *= lead[i]
-    return n if ld is None else ld
+    st = t.stride()
+    if (st[-1] != 1 and inner[-1] != 1) or \
+            (len(inner) == 2 and st[-2] != inner[1] and inner[0] != 1):
+        raise ValueError("%s: the elements of a row must be contiguous" % name)
+    if len(lead) == 1:
+        ld = st[0] if lead[0] != 1 else n
+    else:
+        B, T = lead
+        ld = st[1] if T != 1 else st[0] if B != 1 else n
+        if T != 1 and B != 1 and st[0] != T * ld and ld >= n:
+            raise ValueError("%s: rows must be evenly spaced" % name)
+    if ld < n:
+        raise ValueError("%s: rows must not overlap" % name)
+    return ld
 
 
 def _act(t, name="x"):
@@ -726,7 +733,7 @@ def conv_fwd(x, w, bias=None, s0=None, *, silu: bool = True, lengths=None, y=Non
     with _On(x, stream) as s:
         D, W, args = _conv_args(x, w, bias, s0, lengths, (B, T))
         if y is None:
-            y = torch.empty((B, T, D), dtype=dt, device=dev)
+            y = _like(x)
         if sT is None and return_state:
             sT = torch.empty((B, W - 1, D), dtype=dt, device=dev)
         st = _native.lib().kla_conv_fwd(
@@ -749,7 +756,7 @@ def conv_bwd(x, w, grad_y, bias=None, s0=None, grad_sT=None, *, silu: bool = Tru
         pg = _p(grad_y, "grad_y", dt, (B, T, D), dev)
         ps = _p(grad_sT, "grad_sT", dt, (B, W - 1, D), dev)
         f32 = dict(dtype=torch.float32, device=dev)
-        out = dict(dx=torch.empty((B, T, D), dtype=dt, device=dev),
+        out = dict(dx=_like(x),
                    dw=torch.empty((D, W), **f32),
                    dbias=None if bias is None else torch.empty((D,), **f32),
                    ds0=torch.empty((B, W - 1, D), dtype=dt, device=dev) if need_s0 else None)
@@ -771,7 +778,7 @@ def conv_step(x, w, state, bias=None, *, silu: bool = True, y=None, stream=None)
     with _On(x, stream) as s:
         D, W, args = _conv_args(x, w, bias, state, None, (B,))
         if y is None:
-            y = torch.empty((B, D), dtype=dt, device=dev)
+            y = _like(x)
         st = _native.lib().kla_conv_step(*args[:5], _p(y, "y", dt, (B, D), dev), B, D, W,
                                          bool(silu), _DT[dt], s)
     _check(st, "kla_conv_step")
@@ -825,7 +832,7 @@ def ssm_fwd(u, dt, A, Bm, Cm, D=None, z=None, dt_bias=None, h0=None, *, softplus
     with _On(u, stream) as s:
         Dn, G, N, lds, args = _ssm_args(u, dt, A, Bm, Cm, D, z, dt_bias, (B, T))
         if y is None:
-            y = torch.empty((B, T, Dn), dtype=ty, device=dev)
+            y = _like(u)
         if hT is None and return_state:
             hT = torch.empty((B, Dn, N), dtype=f32, device=dev)
         workspace, nws = _scratch(workspace, ssm_fwd_workspace_size(B, T, Dn, G, N), dev)
@@ -854,14 +861,10 @@ def ssm_bwd(u, dt, A, Bm, Cm, grad_y, D=None, z=None, dt_bias=None, h0=None, gra
                 _p(lengths, "lengths", torch.int32, (B,), dev),
                 _p(grad_y, "grad_y", ty, (B, T, Dn), dev),
                 _p(grad_hT, "grad_hT", torch.float32, (B, Dn, N), dev))
-        act = dict(dtype=ty, device=dev)
         f32 = dict(dtype=torch.float32, device=dev)
-        out = dict(du=torch.empty((B, T, Dn), **act), ddt=torch.empty((B, T, Dn), **act),
-                   dA=torch.empty((Dn, N), **f32), dB=torch.empty((B, T, G, N), **act),
-                   dC=torch.empty((B, T, G, N), **act),
-                   dD=None if D is None else torch.empty((Dn,), **f32),
-                   dz=None if z is None else torch.empty((B, T, Dn), **act),
-                   ddt_bias=None if dt_bias is None else torch.empty((Dn,), **f32),
+        out = dict(du=_like(u), ddt=_like(u), dA=_like(A), dB=_like(Bm), dC=_like(Bm),
+                   dD=None if D is None else _like(D), dz=None if z is None else _like(u),
+                   ddt_bias=None if dt_bias is None else _like(dt_bias),
                    dh0=torch.empty((B, Dn, N), **f32) if need_h0 else None)
         workspace, nws = _scratch(workspace, ssm_bwd_workspace_size(B, T, Dn, G, N), dev)
         st = _native.lib().kla_ssm_bwd(
@@ -883,7 +886,7 @@ def ssm_step(u, dt, A, Bm, Cm, state, D=None, z=None, dt_bias=None, *, softplus:
     with _On(u, stream) as s:
         Dn, G, N, lds, args = _ssm_args(u, dt, A, Bm, Cm, D, z, dt_bias, (B,))
         if y is None:
-            y = torch.empty((B, Dn), dtype=ty, device=dev)
+            y = _like(u)
         st = _native.lib().kla_ssm_step(
             *args, _p(state, "state", torch.float32, (B, Dn, N), dev),
             _p(y, "y", ty, (B, Dn), dev), B, Dn, G, N, *lds, bool(softplus), _DT[ty], s)
@@ -946,9 +949,9 @@ def qk_norm_fwd(q, k, *, wq=None, wk=None, positions=None, inv_freq=None, pos0: 
         (B, T, Hq, Hk, d, _), head, freq = _qk_args(q, k, wq, wk, positions, inv_freq, norm,
                                                      pos0)
         if oq is None:
-            oq = torch.empty(q.shape, dtype=ty, device=dev)
+            oq = _like(q)
         if ok is None:
-            ok = torch.empty(k.shape, dtype=ty, device=dev)
+            ok = _like(k)
         st = _native.lib().kla_qk_norm_fwd(
             *head, pos0, *freq, bool(interleaved), scale, _NORMS[norm], eps,
             _p(oq, "oq", ty, q.shape, dev), _p(ok, "ok", ty, k.shape, dev), B, T, Hq, Hk, d,
@@ -970,10 +973,8 @@ def qk_norm_bwd(q, k, grad_oq, grad_ok, *, wq=None, wk=None, positions=None, inv
         _need_all(grad_ok, "grad_ok")
         gq, gk = _p(grad_oq, "grad_oq", ty, q.shape, dev), _p(grad_ok, "grad_ok", ty, k.shape,
                                                               dev)
-        out = dict(dq=torch.empty(q.shape, dtype=ty, device=dev),
-                   dk=torch.empty(k.shape, dtype=ty, device=dev),
-                   dwq=None if wq is None else torch.empty_like(wq),
-                   dwk=None if wk is None else torch.empty_like(wk))
+        out = dict(dq=_like(q), dk=_like(k), dwq=None if wq is None else _like(wq),
+                   dwk=None if wk is None else _like(wk))
         need = 0
         if wq is not None or wk is not None:
             need = qk_norm_bwd_workspace_size(B, T, Hq, Hk, d, rot)

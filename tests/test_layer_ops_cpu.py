@@ -255,9 +255,11 @@ def test_host_tensors_are_refused(name):
 ])
 def test_row_pitch(make, lead, want, monkeypatch):
     t = make()
+    dev = torch.device("cuda", 0)  # nothing here touches a device
     monkeypatch.setattr(torch.Tensor, "is_cuda", True, raising=False)
+    monkeypatch.setattr(torch.Tensor, "get_device", lambda self: 0)
     if want is None:
         with pytest.raises(ValueError):
-            api._rows(t, "t", torch.float32, lead, (8,), t.device)
+            api._rows(t, "t", torch.float32, lead, (8,), dev)
     else:
-        assert api._rows(t, "t", torch.float32, lead, (8,), t.device) == want
+        assert api._rows(t, "t", torch.float32, lead, (8,), dev) == want
