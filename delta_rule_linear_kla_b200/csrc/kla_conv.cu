@@ -124,6 +124,13 @@ __device__ __forceinline__ void taps_sum(const f32x2 (&tap)[W][kPairs<V>],
   }
 }
 
+// SiLU of a pair (value by value: the packed form takes registers that the
+// prompt's kernel does not have, 57 us instead of 53 for 8 x 4096 x 2048)
+__device__ __forceinline__ f32x2 activate(f32x2 p) {
+  const float2 v = unpack2(p);
+  return pack2(silu(v.x), silu(v.y));
+}
+
 template <int V, int W>
 __device__ __forceinline__ void shift(f32x2 (&win)[W - 1][kPairs<V>],
                                       const f32x2 (&cur)[kPairs<V>]) {
@@ -143,7 +150,7 @@ __device__ __forceinline__ void shift(f32x2 (&win)[W - 1][kPairs<V>],
 // hold neighbouring channels.  Four rows are in flight while the four before
 // are computed, on packed pairs of channels.  Blocks of 128 threads at 72
 // registers, 28 warps an SM, carry enough loads: 8 x 4096 x 2048 bf16 takes
-// 57 us, 4.7 TB/s (64 us with 256 threads at 64 registers, 107 us with eight
+// 53 us, 5.0 TB/s (64 us with 256 threads at 64 registers, 107 us with eight
 // channels a thread).
 constexpr int kFT = 128;
 template <typename T, int V, int W, bool SILU>
@@ -189,10 +196,7 @@ conv_fwd_kernel(const T* __restrict__ x, long long ldx, const float* __restrict_
     shift<V, W>(win, cur);
     if (SILU)
 #pragma unroll
-      for (int i = 0; i < P; ++i) {
-        const float2 v = unpack2(p[i]);
-        p[i] = pack2(silu(v.x), silu(v.y));
-      }
+      for (int i = 0; i < P; ++i) p[i] = activate(p[i]);
     Row<T, V> o;
     o.set(p);
     o.store(to);
@@ -303,10 +307,9 @@ conv_bwd_kernel(const T* __restrict__ x, long long ldx, const float* __restrict_
         f32x2 p[P];
         taps_sum<V, W>(tap, b0, win, cur, p);
 #pragma unroll
-        for (int i = 0; i < P; ++i) {
-          const float2 v = unpack2(p[i]);
-          const f32x2 s = pack2(sigmoid(v.x), sigmoid(v.y)), one = pack2(1.f, 1.f);
-          dp[i] = mul2(dp[i], mul2(s, fma2(p[i], sub2(one, s), one)));
+        for (int i = 0; i < P; ++i) {  // act' = s + p (s - s^2)
+          const f32x2 s = sigmoid2(p[i]);
+          dp[i] = mul2(dp[i], fma2(p[i], fma2(mul2(s, both(-1.f)), s, s), s));
         }
       }
       if (own) {
@@ -459,10 +462,7 @@ conv_step_kernel(const T* __restrict__ x, long long ldx, const float* __restrict
   taps_sum<V, W>(tap, b0, win, cur, p);
   if (SILU)
 #pragma unroll
-    for (int i = 0; i < P; ++i) {
-      const float2 v = unpack2(p[i]);
-      p[i] = pack2(silu(v.x), silu(v.y));
-    }
+    for (int i = 0; i < P; ++i) p[i] = activate(p[i]);
   Row<T, V> o;
   o.set(p);
   o.store(y + b * D + c);
@@ -483,8 +483,8 @@ static int fwd_walk(long long B, int T, int CG) {
 }
 
 // Tokens of one backward walk (a block runs kBY of them side by side): 64
-// where that gives every SM four blocks (4 x 8192 x 2048 bf16: 108 us with 64,
-// 118 with 32), 32 where two, and 8 for less.
+// where that gives every SM four blocks (4 x 8192 x 2048 bf16: 102 us with 64,
+// 112 with 32), 32 where two, and 8 for less.
 static int bwd_walk(long long B, int T, int D, int V) {
   const long long cb = (D + kBX * V - 1) / (kBX * V);
   auto blocks = [&](int L) { return B * cb * ((T + L * kBY - 1) / (L * kBY)); };
