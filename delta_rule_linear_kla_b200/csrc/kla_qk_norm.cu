@@ -52,13 +52,11 @@ struct Raw8<__nv_bfloat16> {
     r = *reinterpret_cast<const uint4*>(p);
   }
   __device__ __forceinline__ void zero() { r = make_uint4(0, 0, 0, 0); }
-  __device__ __forceinline__ void get(float (&f)[8]) const {
+  __device__ __forceinline__ void get(f32x2 (&f)[4]) const {
     const uint32_t u[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      f[2 * i] = __uint_as_float(u[i] << 16);
-      f[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
-    }
+    for (int i = 0; i < 4; ++i)
+      f[i] = pack2(__uint_as_float(u[i] << 16), __uint_as_float(u[i] & 0xffff0000u));
   }
 };
 template <>
@@ -69,27 +67,24 @@ struct Raw8<float> {
     b = reinterpret_cast<const float4*>(p)[1];
   }
   __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
-  __device__ __forceinline__ void get(float (&f)[8]) const {
-    f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
-    f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+  __device__ __forceinline__ void get(f32x2 (&f)[4]) const {
+    f[0] = pack2(a.x, a.y); f[1] = pack2(a.z, a.w);
+    f[2] = pack2(b.x, b.y); f[3] = pack2(b.z, b.w);
   }
 };
-template <typename T>
-__device__ __forceinline__ void store8(T* p, const float (&f)[8]);
-template <>
-__device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&f)[8]) {
+__device__ __forceinline__ void store8(__nv_bfloat16* p, const f32x2 (&f)[4]) {
   uint32_t u[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+    const float2 v = unpack2(f[i]);
+    __nv_bfloat162 h = __floats2bfloat162_rn(v.x, v.y);
     u[i] = *reinterpret_cast<uint32_t*>(&h);
   }
   *reinterpret_cast<uint4*>(p) = make_uint4(u[0], u[1], u[2], u[3]);
 }
-template <>
-__device__ __forceinline__ void store8(float* p, const float (&f)[8]) {
-  reinterpret_cast<float4*>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
-  reinterpret_cast<float4*>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
+__device__ __forceinline__ void store8(float* p, const f32x2 (&f)[4]) {
+  reinterpret_cast<float4*>(p)[0] = flat(Quad{f[0], f[1]});
+  reinterpret_cast<float4*>(p)[1] = flat(Quad{f[2], f[3]});
 }
 
 // How the partner of a channel is reached: PAIR (2i, 2i+1) lies in the lane,
@@ -118,13 +113,11 @@ __device__ __forceinline__ void make_angles(const Args& p, long long tok0, int n
   }
 }
 
-// This lane's part of its token's angles: co[e], si[e] are what channel c + e
-// and its partner are multiplied with (PAIR: one of each for two channels).
-// Channels that are not turned get (1, 0).
+// This lane's part of its token's angles, for pairs of neighbouring channels:
+// out = v co + o si, o the partners.  Channels that are not turned have (1, 0).
 template <int REACH>
 struct Turn {
-  static constexpr int M = REACH == PAIR ? 4 : 8;
-  float co[M], si[M];
+  f32x2 co[4], si[4];
   int from;  // LANE: the partner's lane
 
   __device__ __forceinline__ void load(const Args& p, int c, const float* cosv,
@@ -132,67 +125,113 @@ struct Turn {
     const int half = p.rot / 2, lane = threadIdx.x & 31;
     from = lane;
 #pragma unroll
-    for (int e = 0; e < M; ++e) { co[e] = 1.f; si[e] = 0.f; }
+    for (int e = 0; e < 4; ++e) {
+      co[e] = both(1.f);
+      si[e] = both(0.f);
+    }
     if constexpr (REACH == PAIR) {
 #pragma unroll
       for (int e = 0; e < 4; ++e)
         if (c + 2 * e < p.rot) {
-          co[e] = cosv[c / 2 + e];
-          si[e] = sinv[c / 2 + e];
+          const float s = sinv[c / 2 + e];
+          co[e] = both(cosv[c / 2 + e]);
+          si[e] = pack2(-s, s);
         }
-    } else {
-      if constexpr (REACH == LANE) {
-        if (c < p.rot) from = c < half ? lane + half / 8 : lane - half / 8;
-      }
+    } else if constexpr (REACH == LANE) {  // half a multiple of 8: all 8 on one side
+      if (c < p.rot) {
+        const bool lo = c < half;
+        from = lo ? lane + half / 8 : lane - half / 8;
+        const float4* pc = reinterpret_cast<const float4*>(cosv + (lo ? c : c - half));
+        const float4* ps = reinterpret_cast<const float4*>(sinv + (lo ? c : c - half));
+        const f32x2 sign = both(lo ? -1.f : 1.f);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const int i = c + e;
-        if (i < p.rot) {
-          co[e] = cosv[i < half ? i : i - half];
-          si[e] = i < half ? -sinv[i] : sinv[i - half];
+        for (int j = 0; j < 2; ++j) {
+          const Quad q = quad(pc[j]), r = quad(ps[j]);
+          co[2 * j] = q.a; co[2 * j + 1] = q.b;
+          si[2 * j] = mul2(r.a, sign); si[2 * j + 1] = mul2(r.b, sign);
         }
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        float q[2] = {1.f, 1.f}, r[2] = {0.f, 0.f};
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int i = c + 2 * e + k;
+          if (i < p.rot) {
+            q[k] = cosv[i < half ? i : i - half];
+            r[k] = i < half ? -sinv[i] : sinv[i - half];
+          }
+        }
+        co[e] = pack2(q[0], q[1]);
+        si[e] = pack2(r[0], r[1]);
       }
     }
   }
 
-  // v turned (SIGN 1) or turned back (SIGN -1); row: d floats of staging (SMEM)
-  template <int SIGN>
-  __device__ __forceinline__ void apply(float (&v)[8], const Args& p, int c, float* row) const {
+  // v turned; the backward pass turns back with si's sign flipped beforehand.
+  // row: d floats of staging (SMEM)
+  __device__ __forceinline__ void apply(f32x2 (&v)[4], const Args& p, int c, float* row) const {
+    f32x2 o[4];
     if constexpr (REACH == PAIR) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const float a = v[2 * e], b = v[2 * e + 1], s = SIGN * si[e];
-        v[2 * e] = fmaf(a, co[e], -b * s);
-        v[2 * e + 1] = fmaf(b, co[e], a * s);
+        const float2 a = unpack2(v[e]);
+        o[e] = pack2(a.y, a.x);
       }
     } else if constexpr (REACH == LANE) {
-      float o[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) o[e] = __shfl_sync(0xffffffffu, v[e], from);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = fmaf(v[e], co[e], o[e] * (SIGN * si[e]));
-    } else if constexpr (REACH == SMEM) {
+      for (int e = 0; e < 4; ++e) {
+        const float2 a = unpack2(v[e]);
+        o[e] = pack2(__shfl_sync(0xffffffffu, a.x, from), __shfl_sync(0xffffffffu, a.y, from));
+      }
+    } else {
       const int half = p.rot / 2;
       if (c < p.d)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) row[c + e] = v[e];
+        for (int e = 0; e < 4; ++e) *reinterpret_cast<f32x2*>(row + c + 2 * e) = v[e];
       __syncwarp();
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const int i = c + e;
-        if (i < p.rot)
-          v[e] = fmaf(v[e], co[e], row[i < half ? i + half : i - half] * (SIGN * si[e]));
+      for (int e = 0; e < 4; ++e) {
+        float q[2] = {0.f, 0.f};
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int i = c + 2 * e + k;
+          if (i < p.rot) q[k] = row[i < half ? i + half : i - half];
+        }
+        o[e] = pack2(q[0], q[1]);
       }
       __syncwarp();
     }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = fma2(v[e], co[e], mul2(o[e], si[e]));
+  }
+  __device__ __forceinline__ void reverse() {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) si[e] = mul2(si[e], both(-1.f));
   }
 };
 template <>
 struct Turn<NONE> {
   __device__ __forceinline__ void load(const Args&, int, const float*, const float*) {}
-  template <int SIGN>
-  __device__ __forceinline__ void apply(float (&)[8], const Args&, int, float*) const {}
+  __device__ __forceinline__ void apply(f32x2 (&)[4], const Args&, int, float*) const {}
+  __device__ __forceinline__ void reverse() {}
 };
+
+__device__ __forceinline__ float rsqrt_ftz(float x) {
+  float y;
+  asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// sum of a lane's eight products, then of the row's lanes
+template <int LPR>
+__device__ __forceinline__ float row_dot(const f32x2 (&a)[4], const f32x2 (&b)[4]) {
+  const float2 s = unpack2(fma2(a[3], b[3], fma2(a[2], b[2], fma2(a[1], b[1], mul2(a[0], b[0])))));
+  float r = s.x + s.y;
+#pragma unroll
+  for (int o = LPR / 2; o > 0; o >>= 1) r += __shfl_xor_sync(0xffffffffu, r, o);
+  return r;
+}
 
 // LPR lanes a row; a block has kNT / LPR row places, TB tokens of them with
 // the same number of places each.  BWD: q and k with their gradients to dq,
@@ -204,14 +243,16 @@ qk_kernel(Args p, long long ntiles) {
   constexpr int U = BWD || sizeof(T) == 4 ? 2 : 4;  // rows loaded ahead
   __shared__ __align__(16) float s_cos[REACH == NONE ? 1 : kTrig];
   __shared__ __align__(16) float s_sin[REACH == NONE ? 1 : kTrig];
-  __shared__ float s_row[REACH == SMEM ? RPB : 1][REACH == SMEM ? LPR * 8 : 1];
+  __shared__ __align__(16) float s_row[REACH == SMEM ? RPB : 1][REACH == SMEM ? LPR * 8 : 1];
   const int lr = threadIdx.x % LPR, rr = threadIdx.x / LPR, c = lr * 8;
   const int places = RPB / p.TB;  // of a token
   const int tt = rr / places, h0 = rr - tt * places;
   const int H = p.Hq + p.Hk;
   const float inv_m = p.norm == 2 ? 1.f / (float)p.d : 1.f;
   float* const row = s_row[REACH == SMEM ? rr : 0];
-  float aq[BWD ? 8 : 1] = {}, ak[BWD ? 8 : 1] = {};
+  f32x2 aq[4], ak[4];  // BWD: sums of the weights' gradients
+#pragma unroll
+  for (int e = 0; e < 4; ++e) aq[e] = ak[e] = both(0.f);
   __shared__ __align__(16) float s_w[2][LPR * 8];
   const bool weighted = p.wq || p.wk;
   if (weighted) {
@@ -221,12 +262,12 @@ qk_kernel(Args p, long long ntiles) {
     }
     __syncthreads();
   }
-  auto times_w = [&](float (&v)[8], bool isq) {
+  auto times_w = [&](f32x2 (&v)[4], bool isq) {
     if (!weighted) return;
     const float4* w = reinterpret_cast<const float4*>(&s_w[isq ? 0 : 1][c]);
-    const float4 a = w[0], b = w[1];
-    v[0] *= a.x; v[1] *= a.y; v[2] *= a.z; v[3] *= a.w;
-    v[4] *= b.x; v[5] *= b.y; v[6] *= b.z; v[7] *= b.w;
+    const Quad a = quad(w[0]), b = quad(w[1]);
+    v[0] = mul2(v[0], a.a); v[1] = mul2(v[1], a.b);
+    v[2] = mul2(v[2], b.a); v[3] = mul2(v[3], b.b);
   };
   // a token's rows, in bytes from each array's start: head h of q, or head h -
   // Hq of k, lies h * d elements on (k's starts are set back by Hq heads)
@@ -248,7 +289,7 @@ qk_kernel(Args p, long long ntiles) {
   };
   auto at = [&](const void* q, const void* k, long long qo, long long ko, int h) {
     const char* a = h < p.Hq ? (const char*)q + qo : (const char*)k + ko;
-    return (T*)(a + (long long)(h * p.d) * es);
+    return (T*)(a + (unsigned)(h * p.d * (int)es));  // below 2^31: h < 2^20, d <= 256
   };
   Raw8<T> xn[U], gn[BWD ? U : 1];  // the rows to come
   auto load = [&](const Where& w, int hb) {  // heads hb + h0, one place apart
@@ -268,7 +309,8 @@ qk_kernel(Args p, long long ntiles) {
   for (long long tile = blockIdx.x; tile < ntiles; tile += gridDim.x) {  // forward: once
     const long long tok0 = tile * p.TB;
     const int nt = (int)min((long long)p.TB, p.tokens - tok0);
-    const Where wn = where(tile + gridDim.x);
+    Where wn = w;
+    if constexpr (BWD) wn = where(tile + gridDim.x);
     Turn<REACH> turn;
     if constexpr (REACH != NONE) {
       if (tile != blockIdx.x) __syncthreads();  // the last tile's angles are read
@@ -276,6 +318,7 @@ qk_kernel(Args p, long long ntiles) {
       __syncthreads();
       const int mine_at = tt < nt ? tt * (p.rot / 2) : 0;
       turn.load(p, c, s_cos + mine_at, s_sin + mine_at);
+      if (BWD) turn.reverse();
     }
     // every thread makes as many passes: all lanes take part in the exchanges
     for (int hb = 0; hb < H; hb += U * places) {
@@ -299,44 +342,33 @@ qk_kernel(Args p, long long ntiles) {
         if (hb + i * places >= H) break;  // the same for all threads
         const int hh = hb + i * places + h0;
         const bool live = w.mine && hh < H, isq = hh < p.Hq;
-        float v[8], r = 1.f;
+        f32x2 v[4];
+        float r = 1.f;
         x[i].get(v);
         if (p.norm) {
-          float ss = 0.f;
+          r = rsqrt_ftz(fmaf(row_dot<LPR>(v, v), inv_m, p.eps));
 #pragma unroll
-          for (int e = 0; e < 8; ++e) ss = fmaf(v[e], v[e], ss);
-#pragma unroll
-          for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-          r = rsqrtf(fmaf(ss, inv_m, p.eps));
+          for (int e = 0; e < 4; ++e) v[e] = mul2(v[e], both(r));
         }
         if constexpr (!BWD) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) v[e] *= r;
           times_w(v, isq);
-          turn.template apply<1>(v, p, c, row);
+          turn.apply(v, p, c, row);
           if (live) store8(at(p.oq, p.ok, w.q_out, w.k_out, hh), v);
         } else {
-          float d[8];
+          f32x2 d[4];
           g[i].get(d);
-          turn.template apply<-1>(d, p, c, row);
-          float dot = 0.f;
+          turn.apply(d, p, c, row);
+          if (isq)
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            v[e] *= r;
-            if (isq)
-              aq[e] = fmaf(d[e], v[e], aq[e]);
-            else
-              ak[e] = fmaf(d[e], v[e], ak[e]);
-          }
+            for (int e = 0; e < 4; ++e) aq[e] = fma2(d[e], v[e], aq[e]);
+          else
+#pragma unroll
+            for (int e = 0; e < 4; ++e) ak[e] = fma2(d[e], v[e], ak[e]);
           times_w(d, isq);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) dot = fmaf(d[e], v[e], dot);
           if (p.norm) {
+            const f32x2 dot = both(-inv_m * row_dot<LPR>(d, v));
 #pragma unroll
-            for (int o = LPR / 2; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
-            dot *= inv_m;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) d[e] = r * fmaf(-v[e], dot, d[e]);
+            for (int e = 0; e < 4; ++e) d[e] = mul2(both(r), fma2(v[e], dot, d[e]));
           }
           if (live) store8(at(p.oq, p.ok, w.q_out, w.k_out, hh), d);
         }
@@ -347,12 +379,13 @@ qk_kernel(Args p, long long ntiles) {
   if constexpr (BWD) {
     if (!p.part) return;
     // over the block's rows in order, 8 KB at a time
-    __shared__ float s_sum[RPB][LPR * 8];
+    __shared__ __align__(16) float s_sum[RPB][LPR * 8];
 #pragma unroll
     for (int w = 0; w < 2; ++w) {
       __syncthreads();
 #pragma unroll
-      for (int e = 0; e < 8; ++e) s_sum[rr][c + e] = w ? ak[e] : aq[e];
+      for (int e = 0; e < 4; ++e)
+        *reinterpret_cast<f32x2*>(&s_sum[rr][c + 2 * e]) = w ? ak[e] : aq[e];
       __syncthreads();
       for (int i = threadIdx.x; i < p.d; i += kNT) {
         float s = 0.f;
@@ -449,7 +482,7 @@ static kla_status check(int B, int T, int Hq, int Hk, int d, int rot, int norm, 
   if ((long long)Hq * d > ldq || (long long)Hk * d > ldk) return KLA_ERR_INVALID_ARG;
   const long long rows = (long long)B * T;
   if (!size_ok(rows, ldq) || !size_ok(rows, ldk)) return KLA_ERR_INVALID_ARG;
-  if (T > kMaxTokens || d % 8 != 0 || d > 256 || Hq > (1 << 20) || Hk > (1 << 20))
+  if (T > kMaxTokens || d % 8 != 0 || d > 256 || Hq > (1 << 19) || Hk > (1 << 19))
     return KLA_ERR_UNSUPPORTED;
   // rows are read 8 channels at a time
   const int v = 16 / elem(dtype);
