@@ -429,20 +429,24 @@ static int lanes(int d) {
   return l;
 }
 
-// Tokens of a block, a power of two: a quarter of a token's heads side by side,
-// so that a thread uses its angles for about four, and all of them (up to the
-// block's places) while the blocks would not give every SM two.
+// Tokens of a block, a power of two.  A thread walks at least 16 heads (or all)
+// of its token, so that its angles serve many rows (8 x 4096 tokens of 8 + 8
+// heads of 128: 48 us with all 16 heads a thread, 55 with 8, 81 with 4); while
+// the blocks would not give every SM two, up to all heads lie side by side.
 static int tokens_per_block(int H, int d, long long tokens) {
   const int places = kNT / lanes(d);
   int side = 1;
-  while (side * 8 <= H && side < places) side *= 2;
+  while (side * 32 <= H && side < places) side *= 2;
   while (side < H && side < places && tokens < 2LL * 148 * (places / side)) side *= 2;
   return places / side;
 }
 
+// The backward pass keeps its sums of the weights' gradients over many tiles:
+// two blocks an SM (4 x 8192 tokens of 32 + 8 heads of 64: 102 us, 107 with
+// four), as many as are resident.
 static long long blocks_of(long long tokens, int TB, bool bwd) {
   const long long n = (tokens + TB - 1) / TB;
-  const long long most = bwd ? 148 * 4 : 0x7fffffffLL;
+  const long long most = bwd ? 148 * 2 : 0x7fffffffLL;
   return n < most ? n : most;
 }
 
