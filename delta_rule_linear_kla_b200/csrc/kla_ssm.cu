@@ -12,17 +12,25 @@
 //
 // What bounds it: one exponential a state element and token.  The special
 // function unit gives 16 a clock and SM, so N = 16 states take a clock of an
-// SM per channel and token, against 8 bytes (u, dt, z, y in bf16): about
-// three times what HBM needs.
+// SM per channel and token, three times what their bytes (u, dt, z, y in bf16)
+// take of HBM.
 //
-// Split: a thread holds 4 states of CPT channels, the N/4 threads of a channel
-// lie side by side in a warp, and a block's channels walk the tokens in tiles.
-// Half of the block's warps run the recurrence; the other half prepare the
-// next tile (softplus, dt' u, B and C to fp32) and finish the previous one
-// (skip, gate, store), so the two kinds of work overlap.  With few channels
-// the sequence is cut into segments: their end states from zero starts in
-// parallel (MODE LOCAL), a short chain over segments, then all of them again
-// from their true starts.
+// Split: a thread holds 4 states of 2 channels (their B and C are read once
+// for both, and packed fp32 does two states an instruction), the N/4 threads
+// of a channel lie side by side in a warp, and a block's channels walk the
+// tokens in tiles.  Some warps run the recurrence; helper warps prepare the
+// next tile (softplus, dt' u) and finish the previous one (skip, gate, store),
+// so the two kinds of work overlap.  With few channels the sequence is cut into
+// segments: their end states from zero starts in parallel (MODE LOCAL), a short
+// chain over segments, then all of them again from their true starts.
+//
+// Measured, 8 x 4096 x 2048 x 16 bf16: 440 us, where the exponentials alone
+// take 235 and with the softplus and the gate 280.  Two blocks an SM keep the
+// special function unit 69 % busy over all SMs (256 blocks on 148), issue slots
+// 52 %, the shared-memory pipe 53 %: a mix in which moving work from one to
+// another lost (operands stored twice, 464 us; B and C kept in bf16, 462; a
+// quarter of the exponentials as polynomials, 464 when the rest took 466).
+// 1 x 4096 x 2048 x 16, cut into segments: 99 us.
 #include "kla_layer.cuh"
 
 namespace kla {
@@ -361,24 +369,12 @@ scan_kernel(Args p) {
           const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(sc + t * N);
           cv[0] = v.x; cv[1] = v.y;
         }
-        float d[CPT], x[CPT];
-        if constexpr (CPT == 4) {
-          const float4 v = *reinterpret_cast<const float4*>(sd + t * CH);
-          const float4 w = *reinterpret_cast<const float4*>(sx + t * CH);
-          d[0] = v.x; d[1] = v.y; d[2] = v.z; d[3] = v.w;
-          x[0] = w.x; x[1] = w.y; x[2] = w.z; x[3] = w.w;
-        } else if constexpr (CPT == 2) {
-          const float2 v = *reinterpret_cast<const float2*>(sd + t * CH);
-          const float2 w = *reinterpret_cast<const float2*>(sx + t * CH);
-          d[0] = v.x; d[1] = v.y;
-          x[0] = w.x; x[1] = w.y;
-        } else {
-          d[0] = sd[t * CH];
-          x[0] = sx[t * CH];
-        }
+        const float2 dv = *reinterpret_cast<const float2*>(sd + t * CH);
+        const float2 xv = *reinterpret_cast<const float2*>(sx + t * CH);
+        const float d[CPT] = {dv.x, dv.y}, x[CPT] = {xv.x, xv.y};
 #pragma unroll
         for (int c = 0; c < CPT; ++c) {
-          const f32x2 d2 = pack2(d[c], d[c]), w2 = pack2(x[c], x[c]);
+          const f32x2 d2 = both(d[c]), w2 = both(x[c]);
           const f32x2 e0 = ex2_2(mul2(d2, a2[c][0])), e1 = ex2_2(mul2(d2, a2[c][1]));
           if (REV) {
             h[c][0] = mul2(e0, fma2(w2, cv[0], h[c][0]));
@@ -471,9 +467,10 @@ chain_kernel(const float* __restrict__ A, const float* __restrict__ h0, float* e
 // exchanged at once.  Sums over channels (dB, dC) cross the other lanes: there
 // register s of a thread holds state s ^ (its place among the channels), from
 // copies of B and C in that order, so that every exchange sends fixed
-// registers and needs no selection.  What bounds it are issue slots (about 140
-// instructions a token for 8 states) and the shared-memory pipe, which these
-// choices lighten.
+// registers and needs no selection.  What bounds it are issue slots (about 170
+// instructions a token for a thread's 8 states, 50 % of the slots used with two
+// recurrence warps a scheduler, which is what the registers allow).
+// 2 x 4096 x 2048 x 16 bf16: 375 us of the pass's 563.
 // dB and dC leave as one part a channel tile, dA, dD and dt_bias as one a
 // segment, and reduce kernels add the parts in order: no atomics, the same
 // bits every time.
