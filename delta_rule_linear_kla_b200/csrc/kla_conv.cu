@@ -158,20 +158,18 @@ __global__ void __launch_bounds__(kFT, 7)
 conv_fwd_kernel(const T* __restrict__ x, long long ldx, const float* __restrict__ w,
                 const float* __restrict__ bias, const T* __restrict__ s0,
                 const int* __restrict__ lengths, T* __restrict__ y, T* __restrict__ sT,
-                int Tn, int D, int CG, int NB, int L, long long total) {
+                int Tn, int D, unsigned CG, unsigned NB, int L, unsigned total) {
   constexpr int P = kPairs<V>;
-  const long long id = (long long)blockIdx.x * kFT + threadIdx.x;
+  const unsigned id = blockIdx.x * kFT + threadIdx.x;
   if (id >= total) return;
-  const int cg = (int)(id % CG);
-  const long long rest = id / CG;
-  const int tb = (int)(rest % NB), b = (int)(rest / NB);
-  const int c = cg * V;
+  const unsigned rest = id / CG, cg = id - rest * CG, b = rest / NB, tb = rest - b * NB;
+  const int c = (int)cg * V;
   const int n = live_tokens(lengths, b, Tn);
   const T* xb = x + (long long)b * Tn * ldx + c;
   const T* s0b = s0 ? s0 + (long long)b * (W - 1) * D + c : nullptr;
   T* yb = y + (long long)b * Tn * D + c;
 
-  const int t0 = tb * L, t1 = min(Tn, t0 + L), tn = min(t1, n);
+  const int t0 = (int)tb * L, t1 = min(Tn, t0 + L), tn = min(t1, n);
   Row<T, V> next[4];
   auto fetch = [&](int t) {
     const T* px = xb + (long long)t * ldx;
@@ -445,11 +443,11 @@ template <typename T, int V, int W, bool SILU>
 __global__ void __launch_bounds__(128)
 conv_step_kernel(const T* __restrict__ x, long long ldx, const float* __restrict__ w,
                  const float* __restrict__ bias, T* __restrict__ s, T* __restrict__ y, int D,
-                 int CG, long long total) {
-  const long long id = (long long)blockIdx.x * 128 + threadIdx.x;
+                 unsigned CG, unsigned total) {
+  const unsigned id = blockIdx.x * 128 + threadIdx.x;
   if (id >= total) return;
-  const int c = (int)(id % CG) * V;
   const long long b = id / CG;
+  const int c = (int)(id - (unsigned)b * CG) * V;
   T* sb = s + b * (W - 1) * D + c;
   Row<T, V> rows[W];
 #pragma unroll
@@ -504,10 +502,11 @@ static cudaError_t launch_fwd(const void* x, long long ldx, const float* w, cons
                               int Tn, int D, bool silu, cudaStream_t st) {
   const int CG = D / V, L = fwd_walk(B, Tn, CG), NB = (Tn + L - 1) / L;
   const long long total = (long long)B * NB * CG, blocks = (total + kFT - 1) / kFT;
-  if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
+  // (more threads than 32 bits count would need more memory than there is)
+  if (total > 0xffffff00LL) return cudaErrorInvalidValue;
   auto k = silu ? conv_fwd_kernel<T, V, W, true> : conv_fwd_kernel<T, V, W, false>;
   k<<<(unsigned)blocks, kFT, 0, st>>>((const T*)x, ldx, w, bias, (const T*)s0, lengths, (T*)y,
-                                      (T*)sT, Tn, D, CG, NB, L, total);
+                                      (T*)sT, Tn, D, CG, NB, L, (unsigned)total);
   return cudaGetLastError();
 }
 
@@ -536,9 +535,10 @@ static cudaError_t launch_step(const void* x, long long ldx, const float* w, con
                                void* s, void* y, int B, int D, bool silu, cudaStream_t st) {
   const int CG = D / V;
   const long long total = (long long)B * CG, blocks = (total + 127) / 128;
-  if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
+  if (total > 0xffffff00LL) return cudaErrorInvalidValue;
   auto k = silu ? conv_step_kernel<T, V, W, true> : conv_step_kernel<T, V, W, false>;
-  k<<<(unsigned)blocks, 128, 0, st>>>((const T*)x, ldx, w, bias, (T*)s, (T*)y, D, CG, total);
+  k<<<(unsigned)blocks, 128, 0, st>>>((const T*)x, ldx, w, bias, (T*)s, (T*)y, D, CG,
+                                      (unsigned)total);
   return cudaGetLastError();
 }
 
