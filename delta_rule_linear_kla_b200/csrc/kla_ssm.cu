@@ -28,8 +28,9 @@
 // take 235 and with the softplus and the gate 280.  Two blocks an SM keep the
 // special function unit 69 % busy over all SMs (256 blocks on 148), issue slots
 // 52 %, the shared-memory pipe 53 %: a mix in which moving work from one to
-// another lost (operands stored twice, 464 us; B and C kept in bf16, 462; a
-// quarter of the exponentials as polynomials, 464 when the rest took 466).
+// another lost (operands stored twice, 464 us; B and C kept in bf16, 462; an
+// eighth or a quarter of the exponentials as polynomials, 464 and 481 when all
+// on the special function unit took 466).
 // 1 x 4096 x 2048 x 16, cut into segments: 99 us.
 #include "kla_layer.cuh"
 
