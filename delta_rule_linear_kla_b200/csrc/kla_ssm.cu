@@ -143,7 +143,8 @@ scan_kernel(Args p) {
   const int nc = min(CH, (g + 1) * Dg - c0);     // channels that exist
   const int t_lo = sg * p.seg, t_hi = min(p.T, t_lo + p.seg);
   const int t_live = min(t_hi, live_tokens(p.lengths, b, p.T));
-  const int ntile = (t_hi - t_lo + TK - 1) / TK;
+  // tiles with tokens that exist; those behind leave the state as it is
+  const int ntile = t_live > t_lo ? (t_live - t_lo + TK - 1) / TK : 0;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int first = REV ? ntile - 1 : 0, dir = REV ? -1 : 1;
   const long long row0 = (long long)b * p.T;
@@ -292,7 +293,12 @@ scan_kernel(Args p) {
       if (i + 2 < ntile) load(k + 2 * dir);
       __syncthreads();
     }
-    if (MODE == FULL && ntile > 0) finish(ntile - 1, xp, zp);
+    if (MODE == FULL) {
+      if (ntile > 0) finish(ntile - 1, xp, zp);
+      if (m > 0)
+        for (int t = t_lo + ntile * TK + tt0; t < t_hi; t += TS)
+          st4(y + (long long)t * p.D, make_float4(0.f, 0.f, 0.f, 0.f), m, vec);
+    }
     return;
   }
 
@@ -443,7 +449,8 @@ chain_kernel(const float* __restrict__ A, const float* __restrict__ h0, float* e
     for (int j = 0; j < 8; ++j) {
       const int i = i0 + j, s = REV ? S - 1 - i : i;
       if (i < S) ends[(b * S + s) * dn + at] = h;
-      h = fmaf(ex2(a2 * sum[j]), h, own[j]);
+      // (a state of 0 stays 0 under a growth past fp32's range)
+      h = h == 0.f ? own[j] : fmaf(ex2(a2 * sum[j]), h, own[j]);
     }
   }
 }
@@ -574,7 +581,9 @@ bwd_kernel(BwdArgs q) {
   const int nc = min(CH, (g + 1) * Dg - c0);
   const int t_lo = sg * p.seg, t_hi = min(p.T, t_lo + p.seg);
   const int t_live = min(t_hi, live_tokens(p.lengths, b, p.T));
-  const int ntile = (t_hi - t_lo + K - 1) / K;
+  // tiles with tokens that exist: behind them the gradients are zeros, and the
+  // adjoint state comes through as it is
+  const int ntile = t_live > t_lo ? (t_live - t_lo + K - 1) / K : 0;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const long long row0 = (long long)b * p.T;
   const long long ps = (long long)b * p.S + sg;
@@ -708,10 +717,12 @@ bwd_kernel(BwdArgs q) {
         }
       }
     };
-    load(ntile - 1);
-    stage(ntile - 1);
-    cur = next;
-    if (ntile > 1) load(ntile - 2);
+    if (ntile > 0) {
+      load(ntile - 1);
+      stage(ntile - 1);
+      cur = next;
+      if (ntile > 1) load(ntile - 2);
+    }
     __syncthreads();
     for (int k = ntile - 1; k >= 0; --k) {
       if (k + 1 < ntile) finish(k + 1);  // before its buffer is filled anew
@@ -721,7 +732,17 @@ bwd_kernel(BwdArgs q) {
       if (k > 1) load(k - 2);
       __syncthreads();
     }
-    finish(0);
+    if (ntile > 0) finish(0);
+    const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+    const int t_end = t_lo + ntile * K;
+    if (m > 0)
+      for (int t = t_end + tt0; t < t_hi; t += TS < K ? TS : K) {
+        st4(du + (long long)t * p.D, zero, m, vec);
+        st4(ddt + (long long)t * p.D, zero, m, vec);
+        if (has_z) st4(dz + (long long)t * p.D, zero, m, vec);
+      }
+    for (int t = t_end + hid / (N / 2); t < t_hi; t += NH / (N / 2))
+      *reinterpret_cast<float4*>(pbc + (long long)t * p.G * 2 * N + hid % (N / 2) * 4) = zero;
     // dD, ddt_bias: over the threads that kept the same 4 channels, through
     // the other buffer
     float* red = smem + Sh::BUF;
@@ -793,7 +814,7 @@ bwd_kernel(BwdArgs q) {
     }
     cp_commit();
   };
-  fetch(ntile - 1);
+  if (ntile > 0) fetch(ntile - 1);
   __syncthreads();
   for (int k = ntile - 1; k >= 0; --k) {
     float* buf = smem + (k & 1) * Sh::BUF;
@@ -818,8 +839,13 @@ bwd_kernel(BwdArgs q) {
         if (q.fS > 1) {  // saved from a zero start: add what the segment's start left
           const float4 w = reorder(v[(2 + c) * CW * 32], ord);
           const f32x2 s2 = c ? pack2(s.y, s.y) : pack2(s.x, s.x);
-          h0[c][0] = fma2(ex2_2(mul2(s2, a2[c][0])), pack2(w.x, w.y), h0[c][0]);
-          h0[c][1] = fma2(ex2_2(mul2(s2, a2[c][1])), pack2(w.z, w.w), h0[c][1]);
+          const float2 g0 = unpack2(ex2_2(mul2(s2, a2[c][0])));
+          const float2 g1 = unpack2(ex2_2(mul2(s2, a2[c][1])));
+          // (a start of 0 leaves 0 under a growth past fp32's range)
+          h0[c][0] = add2(h0[c][0], pack2(w.x == 0.f ? 0.f : g0.x * w.x,
+                                          w.y == 0.f ? 0.f : g0.y * w.y));
+          h0[c][1] = add2(h0[c][1], pack2(w.z == 0.f ? 0.f : g1.x * w.z,
+                                          w.w == 0.f ? 0.f : g1.y * w.w));
         }
       }
     }

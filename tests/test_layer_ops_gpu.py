@@ -18,6 +18,8 @@ counts the fp32 roundings on the way:
           angle's sine (pi units of 2^-24 and 2 ulp), products: c = 64; backward
           twice that; dw sums over n rows in parts: c = 128 + rows / 16
 """
+import math
+
 import pytest
 import torch
 
@@ -162,6 +164,8 @@ SSM = [  # B, T, D, G, N, dtype, z, skip, bias, softplus, state, lengths, wide
     (1, 41, 33, 1, 32, "bf16", True, True, True, True, True, None, True),
     (1, 1300, 10, 1, 16, "fp32", True, True, True, True, True, None, False),   # segments
     (2, 1100, 6, 2, 8, "bf16", True, True, True, True, True, [1100, 700], False),
+    (3, 1100, 6, 1, 16, "fp32", True, True, True, True, True, [90, 0, 641], False),  # segments
+    # without a token
 ]
 
 
@@ -271,6 +275,32 @@ def test_ssm_extreme_steps():
     y, h = api.ssm_fwd(u, dt, A, Bm, Cm, h0=h0)
     own = 1000.0 * u[:, -1, :, None] * Bm[:, -1]
     assert torch.allclose(h, own, rtol=1e-6) and torch.isfinite(y).all()
+
+
+def test_ssm_growth_leaves_zeros():
+    """A growing channel (A > 0) whose states are still 0 when the growth of
+    the segments before passes fp32's range (e^128 and more): the state is that
+    of the late input, as without a cut.  The gradients of the last tokens and
+    of C are finite too; earlier ones are not (the adjoint state itself passes
+    e^1000 there)."""
+    B, T, D, N = 1, 2000, 16, 8
+    assert api.ssm_fwd_workspace_size(B, T, D, 1, N) > 0  # cut into segments
+    u = torch.zeros(B, T, D, device="cuda")
+    u[:, -3:] = 1.0
+    dt = torch.ones((B, T, D), device="cuda")
+    A = torch.ones(D, N, device="cuda")
+    bc = torch.ones(B, T, 1, N, device="cuda")
+    y, h = api.ssm_fwd(u, dt, A, bc, bc, softplus=False)
+    want = sum(math.exp(i) for i in range(3))
+    assert not y[:, :-3].any()
+    assert torch.allclose(h, torch.full_like(h, want), rtol=1e-6)
+    gy = torch.zeros_like(y)
+    gy[:, -1] = 1.0
+    g = api.ssm_bwd(u, dt, A, bc, bc, gy, softplus=False)
+    du = [N * math.exp(i) for i in (2, 1, 0)]
+    assert torch.allclose(g["du"][0, -3:, 0].cpu(), torch.tensor(du), rtol=1e-6)
+    assert torch.allclose(g["dC"][0, -1], torch.full_like(g["dC"][0, -1], D * want), rtol=1e-6)
+    assert not g["dC"][:, :-1].any()
 
 
 # ------------------------------------------------------- norm and rotation
