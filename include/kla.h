@@ -487,8 +487,8 @@ KLA_API kla_status kla_conv_step(const void *x, long long ldx, const float *w, c
  *
  * kla_ssm_bwd: every gradient for grad_y and grad_hT (nullable = 0); grad_D,
  * grad_dt_bias, grad_h0 nullable (not computed), grad_z needed with z.
- * Workspace kla_ssm_bwd_workspace_size(...): a state every 16 tokens
- * (B * T * D * N / 4 bytes) and parts of the sums over channels and tokens.
+ * Workspace kla_ssm_bwd_workspace_size(...): a state every 8 tokens
+ * (B * T * D * N / 2 bytes) and parts of the sums over channels and tokens.
  * kla_ssm_step: one token for each of B sequences (u, dt, z, y [B][D], Bm, Cm
  * [B][G][N]); state [B][D][N] fp32 moved on in place.
  */

@@ -589,6 +589,51 @@ def test_empty_prompts():
     assert not r["dwq"].any() and r["dq"].shape == q.shape
 
 
+def test_offsets_past_32_bits():
+    """More than 2^31 elements an activation: the last tokens are those of a
+    short prompt that starts from what stands before them."""
+    if torch.cuda.mem_get_info()[0] < 80 << 30:
+        pytest.skip("needs 80 GB of device memory")
+    T, D, N, tail = (1 << 20) + 100, 2048, 8, 300
+    gen = torch.Generator(device="cuda").manual_seed(60)
+    mk = lambda *s: torch.randn(s, generator=gen, device="cuda", dtype=torch.bfloat16)  # noqa: E731
+    x, w = mk(1, T, D), torch.randn(D, 4, generator=gen, device="cuda")
+    assert x.numel() > 1 << 31
+    cut = lambda a: a[:, -tail:].contiguous()  # noqa: E731
+    y, sT = api.conv_fwd(x, w)
+    s0 = x[:, -tail - 3:-tail].contiguous()
+    yt, st = api.conv_fwd(cut(x), w, None, s0)
+    assert torch.equal(y[:, -tail:], yt) and torch.equal(sT, st)
+    del y
+    g = api.conv_bwd(x, w, x)
+    gt = api.conv_bwd(cut(x), w, cut(x), None, s0)
+    assert torch.equal(g["dx"][:, -tail:], gt["dx"])
+    del g
+    # decays of e^-4 a token: 300 tokens before nothing is left
+    A = torch.full((D, N), -8.0, device="cuda")
+    dt = torch.full((1, T, D), 0.5, device="cuda", dtype=torch.bfloat16)
+    bc = mk(1, T, 1, N)
+    args = lambda f: (f(x), f(dt), A, f(bc), f(bc))  # noqa: E731
+    y, h = api.ssm_fwd(*args(lambda a: a), softplus=False)
+    yt, ht = api.ssm_fwd(*args(cut), softplus=False)
+    assert torch.equal(y[:, -50:], yt[:, -50:]) and torch.equal(h, ht)
+    del y
+    g = api.ssm_bwd(*args(lambda a: a), x, softplus=False)
+    gt = api.ssm_bwd(*args(cut), cut(x), softplus=False)
+    for k in ("du", "ddt", "dB", "dC"):
+        assert torch.equal(g[k][:, -50:], gt[k][:, -50:]), k
+    del g, dt, bc
+    q, k = x.view(1, T, 16, 128), x.view(1, T, 16, 128)[:, :, :1].contiguous()
+    f = (10000.0 ** (-torch.arange(64) / 64.0)).cuda()
+    oq, ok = api.qk_norm_fwd(q, k, inv_freq=f)
+    tq, tk = api.qk_norm_fwd(cut(q), cut(k), inv_freq=f, pos0=T - tail)
+    assert torch.equal(oq[:, -tail:], tq) and torch.equal(ok[:, -tail:], tk)
+    del oq
+    g = api.qk_norm_bwd(q, k, q, k, inv_freq=f)
+    gt = api.qk_norm_bwd(cut(q), cut(k), cut(q), cut(k), inv_freq=f, pos0=T - tail)
+    assert torch.equal(g["dq"][:, -tail:], gt["dq"])
+
+
 def test_large_batch_of_single_tokens():
     """More sequences than a launch's y or z extent would take."""
     B, D, N = 70001, 8, 8
