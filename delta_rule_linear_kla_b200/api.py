@@ -634,6 +634,8 @@ class _On:
 
 def _like(t):
     """A new contiguous tensor of t's shape and type."""
+    if t.is_contiguous():
+        return torch.empty_like(t)
     return torch.empty_like(t, memory_format=torch.contiguous_format)
 
 
@@ -642,9 +644,13 @@ def _p(t, name, dtype, shape, dev):
     its words where one fails."""
     if t is None:
         return None
-    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == dev.index
-            and t.shape == shape and t.is_contiguous()):
-        _need(t, name, dtype, shape, dev)
+    try:
+        if t.dtype is dtype and t.get_device() == dev.index and t.shape == shape \
+                and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:  # not a tensor
+        pass
+    _need(t, name, dtype, shape, dev)
     return t.data_ptr()
 
 
@@ -652,8 +658,11 @@ def _rows(t, name, dtype, lead, inner, dev):
     """Elements between the rows of an input that may be rows of a wider
     matrix: shape lead + inner, inner contiguous, rows evenly spaced."""
     shape = lead + inner
-    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == dev.index
-            and t.shape == shape):
+    try:
+        good = t.dtype is dtype and t.get_device() == dev.index and t.shape == shape
+    except AttributeError:  # not a tensor
+        good = False
+    if not good:
         if not isinstance(t, torch.Tensor) or not t.is_cuda:
             raise ValueError("%s must be a CUDA tensor" % name)
         if t.device != dev:
@@ -681,11 +690,21 @@ def _rows(t, name, dtype, lead, inner, dev):
     return ld
 
 
-def _act(t, name="x"):
-    """The activations' type of a call, from its first tensor."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype not in _DT:
+_MOST = (1 << 31) - 1
+
+
+def _head(t, name, dims):
+    """Type, device and shape of a call's first tensor."""
+    try:
+        dt, dev, shape = t.dtype, t.device, tuple(t.shape)
+        good = dt in _DT and t.is_cuda
+    except AttributeError:  # not a tensor
+        good = False
+    if not good:
         raise ValueError("%s must be a CUDA tensor of dtype bfloat16 or float32" % name)
-    return t.dtype
+    if len(shape) != dims or max(shape) > _MOST:
+        raise ValueError("%s must have %d dimensions below 2^31, got %s" % (name, dims, shape))
+    return dt, dev, shape
 
 
 def _scratch(workspace, need, dev):
@@ -697,29 +716,20 @@ def _scratch(workspace, need, dev):
     return workspace, workspace.numel()
 
 
-def _dims(t, name, n):
-    if t.dim() != n or max(t.shape) >= 1 << 31:
-        raise ValueError("%s must have %d dimensions below 2^31, got %s"
-                         % (name, n, tuple(t.shape)))
-    return tuple(t.shape)
-
-
 def conv_bwd_workspace_size(B: int, T: int, D: int, W: int) -> int:
     return int(_native.lib().kla_conv_bwd_workspace_size(B, T, D, W))
 
 
-def _conv_args(x, w, bias, s0, lengths, lead):
-    """Sizes, x's row pitch and the addresses of x .. lengths."""
-    dt, dev = x.dtype, x.device
-    D = x.shape[-1]
+def _conv_args(x, w, bias, s0, lengths, lead, D, dt, dev):
+    """The width, and the arguments x .. lengths of the C calls."""
     if not isinstance(w, torch.Tensor) or w.dim() != 2 or w.shape[0] != D:
         raise ValueError("w must be a [D, W] CUDA tensor with D = %d" % D)
     W = w.shape[1]
     ldx = _rows(x, "x", dt, lead, (D,), dev)
-    return D, W, (x.data_ptr(), ldx, _p(w, "w", torch.float32, (D, W), dev),
-                  _p(bias, "bias", torch.float32, (D,), dev),
-                  _p(s0, "s0", dt, (lead[0], W - 1, D), dev),
-                  _p(lengths, "lengths", torch.int32, (lead[0],), dev))
+    return W, (x.data_ptr(), ldx, _p(w, "w", torch.float32, (D, W), dev),
+               _p(bias, "bias", torch.float32, (D,), dev),
+               _p(s0, "s0", dt, (lead[0], W - 1, D), dev),
+               _p(lengths, "lengths", torch.int32, (lead[0],), dev))
 
 
 def conv_fwd(x, w, bias=None, s0=None, *, silu: bool = True, lengths=None, y=None, sT=None,
@@ -728,10 +738,9 @@ def conv_fwd(x, w, bias=None, s0=None, *, silu: bool = True, lengths=None, y=Non
     [B,T,D] bf16 or fp32 (rows may be part of a wider matrix), w [D,W] fp32
     with W in {2, 3, 4}, bias [D] fp32, s0 [B,W-1,D] the inputs before x,
     lengths [B] int32.  Returns (y, sT), sT the last W-1 inputs."""
-    dt, dev = _act(x), x.device
-    B, T, _ = _dims(x, "x", 3)
+    dt, dev, (B, T, D) = _head(x, "x", 3)
     with _On(x, stream) as s:
-        D, W, args = _conv_args(x, w, bias, s0, lengths, (B, T))
+        W, args = _conv_args(x, w, bias, s0, lengths, (B, T), D, dt, dev)
         if y is None:
             y = _like(x)
         if sT is None and return_state:
@@ -748,11 +757,10 @@ def conv_bwd(x, w, grad_y, bias=None, s0=None, grad_sT=None, *, silu: bool = Tru
     """Gradients of conv_fwd for dL/dy = grad_y and dL/dsT = grad_sT (None =
     0) (kla_conv_bwd).  Returns a dict: dx and ds0 in x's type (ds0 None
     unless need_s0), dw and dbias fp32 (dbias None without a bias)."""
-    dt, dev = _act(x), x.device
-    B, T, _ = _dims(x, "x", 3)
+    dt, dev, (B, T, D) = _head(x, "x", 3)
     _need_all(grad_y, "grad_y")
     with _On(x, stream) as s:
-        D, W, args = _conv_args(x, w, bias, s0, lengths, (B, T))
+        W, args = _conv_args(x, w, bias, s0, lengths, (B, T), D, dt, dev)
         pg = _p(grad_y, "grad_y", dt, (B, T, D), dev)
         ps = _p(grad_sT, "grad_sT", dt, (B, W - 1, D), dev)
         f32 = dict(dtype=torch.float32, device=dev)
@@ -772,15 +780,16 @@ def conv_step(x, w, state, bias=None, *, silu: bool = True, y=None, stream=None)
     """One token of the convolution for each sequence (kla_conv_step): x
     [B,D]; state [B,W-1,D] (conv_fwd's sT) is moved on in place.  Returns y
     [B,D]."""
-    dt, dev = _act(x), x.device
-    B, _ = _dims(x, "x", 2)
+    dt, dev, (B, D) = _head(x, "x", 2)
     _need_all(state, "state")
     with _On(x, stream) as s:
-        D, W, args = _conv_args(x, w, bias, state, None, (B,))
+        W, args = _conv_args(x, w, bias, state, None, (B,), D, dt, dev)
         if y is None:
             y = _like(x)
-        st = _native.lib().kla_conv_step(*args[:5], _p(y, "y", dt, (B, D), dev), B, D, W,
-                                         bool(silu), _DT[dt], s)
+            py = y.data_ptr()
+        else:
+            py = _p(y, "y", dt, (B, D), dev)
+        st = _native.lib().kla_conv_step(*args[:5], py, B, D, W, bool(silu), _DT[dt], s)
     _check(st, "kla_conv_step")
     return y
 
@@ -798,11 +807,9 @@ def ssm_bwd_workspace_size(B: int, T: int, D: int, G: int, N: int) -> int:
     return int(_native.lib().kla_ssm_bwd_workspace_size(B, T, D, G, N))
 
 
-def _ssm_args(u, dt, A, Bm, Cm, D, z, dt_bias, lead):
-    """Sizes, the row pitches of u, dt, Bm, Cm and z, and the addresses of u ..
-    dt_bias, for prompts and single tokens."""
-    ty, dev = u.dtype, u.device
-    Dn = u.shape[-1]
+def _ssm_args(u, dt, A, Bm, Cm, D, z, dt_bias, lead, Dn, ty, dev):
+    """Groups and states, the row pitches of u, dt, Bm, Cm and z, and the
+    addresses of u .. dt_bias, for prompts and single tokens."""
     if not isinstance(A, torch.Tensor) or A.dim() != 2 or A.shape[0] != Dn:
         raise ValueError("A must be a [D, N] CUDA tensor with D = %d" % Dn)
     N = A.shape[1]
@@ -814,7 +821,7 @@ def _ssm_args(u, dt, A, Bm, Cm, D, z, dt_bias, lead):
            _rows(Bm, "Bm", ty, lead, gn, dev), _rows(Cm, "Cm", ty, lead, gn, dev),
            0 if z is None else _rows(z, "z", ty, lead, ch, dev))
     f32 = torch.float32
-    return Dn, G, N, lds, (
+    return G, N, lds, (
         u.data_ptr(), dt.data_ptr(), _p(A, "A", f32, (Dn, N), dev), Bm.data_ptr(),
         Cm.data_ptr(), _p(D, "D", f32, ch, dev), None if z is None else z.data_ptr(),
         _p(dt_bias, "dt_bias", f32, ch, dev))
@@ -827,10 +834,10 @@ def ssm_fwd(u, dt, A, Bm, Cm, D=None, z=None, dt_bias=None, h0=None, *, softplus
     [B,T,D], Bm, Cm [B,T,G,N] bf16 or fp32 (rows may be parts of wider
     matrices), A [D,N], D, dt_bias [D], h0 [B,D,N] fp32, lengths [B] int32;
     N in {8, 16, 32, 64}.  Returns (y, hT)."""
-    ty, dev, f32 = _act(u, "u"), u.device, torch.float32
-    B, T, _ = _dims(u, "u", 3)
+    ty, dev, (B, T, Dn) = _head(u, "u", 3)
+    f32 = torch.float32
     with _On(u, stream) as s:
-        Dn, G, N, lds, args = _ssm_args(u, dt, A, Bm, Cm, D, z, dt_bias, (B, T))
+        G, N, lds, args = _ssm_args(u, dt, A, Bm, Cm, D, z, dt_bias, (B, T), Dn, ty, dev)
         if y is None:
             y = _like(u)
         if hT is None and return_state:
@@ -852,11 +859,10 @@ def ssm_bwd(u, dt, A, Bm, Cm, grad_y, D=None, z=None, dt_bias=None, h0=None, gra
     0) (kla_ssm_bwd).  Returns a dict: du, ddt, dB, dC, dz in u's type, dA,
     dD, ddt_bias, dh0 fp32 (None for inputs that are None; dh0 None unless
     need_h0)."""
-    ty, dev = _act(u, "u"), u.device
-    B, T, _ = _dims(u, "u", 3)
+    ty, dev, (B, T, Dn) = _head(u, "u", 3)
     _need_all(grad_y, "grad_y")
     with _On(u, stream) as s:
-        Dn, G, N, lds, args = _ssm_args(u, dt, A, Bm, Cm, D, z, dt_bias, (B, T))
+        G, N, lds, args = _ssm_args(u, dt, A, Bm, Cm, D, z, dt_bias, (B, T), Dn, ty, dev)
         more = (_p(h0, "h0", torch.float32, (B, Dn, N), dev),
                 _p(lengths, "lengths", torch.int32, (B,), dev),
                 _p(grad_y, "grad_y", ty, (B, T, Dn), dev),
@@ -880,16 +886,17 @@ def ssm_step(u, dt, A, Bm, Cm, state, D=None, z=None, dt_bias=None, *, softplus:
     """One token of the scan for each sequence (kla_ssm_step): u, dt, z
     [B,D], Bm, Cm [B,G,N]; state [B,D,N] fp32 (ssm_fwd's hT) is moved on in
     place.  Returns y [B,D]."""
-    ty, dev = _act(u, "u"), u.device
-    B, _ = _dims(u, "u", 2)
+    ty, dev, (B, Dn) = _head(u, "u", 2)
     _need_all(state, "state")
     with _On(u, stream) as s:
-        Dn, G, N, lds, args = _ssm_args(u, dt, A, Bm, Cm, D, z, dt_bias, (B,))
+        G, N, lds, args = _ssm_args(u, dt, A, Bm, Cm, D, z, dt_bias, (B,), Dn, ty, dev)
         if y is None:
             y = _like(u)
+            py = y.data_ptr()
+        else:
+            py = _p(y, "y", ty, (B, Dn), dev)
         st = _native.lib().kla_ssm_step(
-            *args, _p(state, "state", torch.float32, (B, Dn, N), dev),
-            _p(y, "y", ty, (B, Dn), dev), B, Dn, G, N, *lds, bool(softplus), _DT[ty], s)
+            *args, _p(state, "state", torch.float32, (B, Dn, N), dev), py, B, Dn, G, N, *lds, bool(softplus), _DT[ty], s)
     _check(st, "kla_ssm_step")
     return y
 
@@ -898,21 +905,21 @@ _NORMS = {None: 0, "l2": 1, "rms": 2}
 
 
 def _qk_args(q, k, wq, wk, positions, inv_freq, norm, pos0):
-    """Sizes (B, T, Hq, Hk, d, rot), and the arguments q .. rot of the C calls
-    but for pos0, in two parts around it."""
-    ty, dev = q.dtype, q.device
-    one = q.dim() == 3  # a single token of each sequence: [B, H, d]
-    if q.dim() not in (3, 4) or not isinstance(k, torch.Tensor) or k.dim() != q.dim():
+    """Type, device, sizes (B, T, Hq, Hk, d, rot), and the arguments q .. rot of
+    the C calls but for pos0, in two parts around it."""
+    one = isinstance(q, torch.Tensor) and q.dim() == 3  # a token each: [B, H, d]
+    ty, dev, shape = _head(q, "q", 3 if one else 4)
+    lead, Hq, d = shape[:-2], shape[-2], shape[-1]
+    if not isinstance(k, torch.Tensor) or k.dim() != len(shape):
         raise ValueError("q and k must be CUDA tensors [B, T, H, d] or [B, H, d]")
-    shape = tuple(q.shape)
-    if max(shape) >= 1 << 31:
-        raise ValueError("q must have dimensions below 2^31, got %s" % (shape,))
-    lead, (Hq, d), Hk = shape[:-2], shape[-2:], k.shape[-2]
+    Hk = k.shape[-2]
     B, T = lead[0], 1 if one else lead[1]
     ldq, ldk = _rows(q, "q", ty, lead, (Hq, d), dev), _rows(k, "k", ty, lead, (Hk, d), dev)
     if norm not in _NORMS:
         raise ValueError("norm must be None, 'l2' or 'rms', got %r" % (norm,))
+    f32 = torch.float32
     stride = rot = 0
+    pp = pf = None
     if positions is not None:
         have = tuple(positions.shape)
         if have == lead:
@@ -920,16 +927,15 @@ def _qk_args(q, k, wq, wk, positions, inv_freq, norm, pos0):
         elif one or have != (T,):
             raise ValueError("positions must have shape %s, got %s"
                              % (lead if one else "%s or %s" % (lead, (T,)), have))
-        _p(positions, "positions", torch.int32, have, dev)
+        pp = _p(positions, "positions", torch.int32, have, dev)
     elif not -(1 << 31) <= pos0 <= (1 << 31) - max(T, 1):
         raise ValueError("positions from pos0 = %d on pass 32 bits" % pos0)
     if inv_freq is not None:
         rot = 2 * inv_freq.numel()
-        _p(inv_freq, "inv_freq", torch.float32, inv_freq.shape, dev)
-    f32 = torch.float32
-    return (B, T, Hq, Hk, d, rot), (
+        pf = _p(inv_freq, "inv_freq", f32, inv_freq.shape, dev)
+    return ty, dev, (B, T, Hq, Hk, d, rot), (
         q.data_ptr(), k.data_ptr(), ldq, ldk, _p(wq, "wq", f32, (d,), dev),
-        _p(wk, "wk", f32, (d,), dev), _ptr(positions), stride), (_ptr(inv_freq), rot)
+        _p(wk, "wk", f32, (d,), dev), pp, stride), (pf, rot)
 
 
 def qk_norm_bwd_workspace_size(B: int, T: int, Hq: int, Hk: int, d: int, rot: int) -> int:
@@ -944,18 +950,19 @@ def qk_norm_fwd(q, k, *, wq=None, wk=None, positions=None, inv_freq=None, pos0: 
     channels by position, in one pass (kla_qk_norm_fwd).  norm: "l2", "rms"
     or None; wq, wk [d] fp32; positions int32 [B,T], [T] or (one token) [B],
     None = pos0 + t; inv_freq fp32, None = no rotation.  Returns (oq, ok)."""
-    ty, dev = _act(q, "q"), q.device
+    ty, dev, (B, T, Hq, Hk, d, _), head, freq = _qk_args(q, k, wq, wk, positions, inv_freq,
+                                                         norm, pos0)
     with _On(q, stream) as s:
-        (B, T, Hq, Hk, d, _), head, freq = _qk_args(q, k, wq, wk, positions, inv_freq, norm,
-                                                     pos0)
+        pq, pk = _p(oq, "oq", ty, q.shape, dev), _p(ok, "ok", ty, k.shape, dev)
         if oq is None:
             oq = _like(q)
+            pq = oq.data_ptr()
         if ok is None:
             ok = _like(k)
+            pk = ok.data_ptr()
         st = _native.lib().kla_qk_norm_fwd(
             *head, pos0, *freq, bool(interleaved), scale, _NORMS[norm], eps,
-            _p(oq, "oq", ty, q.shape, dev), _p(ok, "ok", ty, k.shape, dev), B, T, Hq, Hk, d,
-            _DT[ty], s)
+            pq, pk, B, T, Hq, Hk, d, _DT[ty], s)
     _check(st, "kla_qk_norm_fwd")
     return oq, ok
 
@@ -965,10 +972,9 @@ def qk_norm_bwd(q, k, grad_oq, grad_ok, *, wq=None, wk=None, positions=None, inv
                 interleaved: bool = False, scale: float = 1.0, workspace=None, stream=None):
     """Gradients of qk_norm_fwd (kla_qk_norm_bwd).  Returns a dict: dq, dk in
     q's type, dwq, dwk fp32 (None for weights that are None)."""
-    ty, dev = _act(q, "q"), q.device
+    ty, dev, (B, T, Hq, Hk, d, rot), head, freq = _qk_args(q, k, wq, wk, positions, inv_freq,
+                                                           norm, pos0)
     with _On(q, stream) as s:
-        (B, T, Hq, Hk, d, rot), head, freq = _qk_args(q, k, wq, wk, positions, inv_freq, norm,
-                                                     pos0)
         _need_all(grad_oq, "grad_oq")
         _need_all(grad_ok, "grad_ok")
         gq, gk = _p(grad_oq, "grad_oq", ty, q.shape, dev), _p(grad_ok, "grad_ok", ty, k.shape,
