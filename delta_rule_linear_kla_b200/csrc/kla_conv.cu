@@ -239,13 +239,13 @@ conv_fwd_kernel(const T* __restrict__ x, long long ldx, const float* __restrict_
 // once, forming p and dp and emitting dx[t-W+1] at token t; the W-1 tokens
 // behind its own L are formed twice.  dw and dbias are summed in registers,
 // over the block's walks in shared memory, and over blocks by
-// conv_reduce_kernel in a fixed order (no atomics).  4 x 8192 x 2048 bf16: 102 us,
+// conv_reduce_kernel in a fixed order (no atomics).  4 x 8192 x 2048 bf16: 103 us,
 // 3.9 TB/s; about 28 instructions a value (54 % of the issue slots at 16 warps
 // an SM, the registers' limit) hold it above the 62 us of its bytes.
-constexpr int kBX = 32, kBY = 8;  // channel groups x walks of a block
+constexpr int kBX = 32, kBY = 4;  // channel groups x walks of a block
 
 template <typename T, int V, int W, bool SILU>
-__global__ void __launch_bounds__(kBX* kBY)
+__global__ void __launch_bounds__(kBX* kBY, 4)
 conv_bwd_kernel(const T* __restrict__ x, long long ldx, const float* __restrict__ w,
                 const float* __restrict__ bias, const T* __restrict__ s0,
                 const int* __restrict__ lengths, const T* __restrict__ gy,
@@ -482,13 +482,14 @@ static int fwd_walk(long long B, int T, int CG) {
   return 4;
 }
 
-// Tokens of one backward walk (a block runs kBY of them side by side): 64
-// where that gives every SM four blocks (4 x 8192 x 2048 bf16: 102 us with 64,
-// 112 with 32), 32 where two, and 8 for less.
+// Tokens of one backward walk (a block runs kBY of them side by side): the
+// longest that gives every SM the four blocks that it holds (4 x 8192 x 2048
+// bf16: 103 us with 64, 112 with 32; 2 x 8192: 56 and 61), 16 where that gives
+// two, and 8 for less.
 static int bwd_walk(long long B, int T, int D, int V) {
   const long long cb = (D + kBX * V - 1) / (kBX * V);
   auto blocks = [&](int L) { return B * cb * ((T + L * kBY - 1) / (L * kBY)); };
-  return blocks(64) >= 4 * 148 ? 64 : blocks(32) >= 2 * 148 ? 32 : 8;
+  return blocks(64) >= 4 * 148 ? 64 : blocks(32) >= 4 * 148 ? 32 : blocks(16) >= 2 * 148 ? 16 : 8;
 }
 
 static long long bwd_parts(int B, int T, int D, int V) {

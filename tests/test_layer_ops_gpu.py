@@ -7,7 +7,7 @@ counts the fp32 roundings on the way:
 
   conv    W + 1 terms, SiLU's exponential and division (|p| <= 8 here: 2 + 1.2
           |p| and 2 units of 2^-23 each, twice for the derivative): c = 64;
-          sums over tokens (dw, dbias) add at most 32 + 8 + 8 additions and
+          sums over tokens (dw, dbias) add at most 64 + 4 + 8 additions and
           one for each eighth block: c = 64 + 2 * 64
   scan    a step's factor is off by (3 |dt' A| + 4) units (argument, 2-ulp
           exponential) and its input by about 16 (softplus, products); errors
