@@ -117,7 +117,8 @@ __device__ __forceinline__ void make_angles(const Args& p, long long tok0, int n
 }
 
 // This lane's part of its token's angles, for pairs of neighbouring channels:
-// out = v co + o si, o the partners.  Channels that are not turned have (1, 0).
+// out = v co + o si, o the partners.  Channels that are not turned have (1, 0)
+// and partner 0: an infinity beside them, or their own, stays where it is.
 template <int REACH>
 struct Turn {
   f32x2 co[4], si[4];
@@ -180,13 +181,14 @@ struct Turn {
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const float2 a = unpack2(v[e]);
-        o[e] = pack2(a.y, a.x);
+        o[e] = c + 2 * e < p.rot ? pack2(a.y, a.x) : both(0.f);
       }
     } else if constexpr (REACH == LANE) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const float2 a = unpack2(v[e]);
         o[e] = pack2(__shfl_sync(0xffffffffu, a.x, from), __shfl_sync(0xffffffffu, a.y, from));
+        if (c >= p.rot) o[e] = both(0.f);
       }
     } else {
       const int half = p.rot / 2;

@@ -377,6 +377,26 @@ def test_qk_norm_positions():
     check(a[0], ref.head_norm(q, None, pos, f), 68)
 
 
+@pytest.mark.parametrize("dt", ["bf16", "fp32"])
+@pytest.mark.parametrize("rot,interleaved", [(16, False), (12, False), (20, True)])
+def test_channels_that_are_not_turned_stay(rot, interleaved, dt):
+    """Without a norm, channels behind the rotation come out unchanged, in
+    both directions: infinities and NaN too, and none reaches a neighbour."""
+    r = Rand(32)
+    q, g = r.n(2, 5, 3, 64, dt=DT[dt]), r.n(2, 5, 3, 64, dt=DT[dt])
+    for x in (q, g):
+        x[:, :, 0, rot], x[:, 1, :, rot + 3], x[0, 2, :, 40] = math.inf, -math.inf, math.nan
+    q, g = gpu(q, g)
+    f = (10000.0 ** (-torch.arange(rot // 2) * 2.0 / rot)).cuda()
+    kw = dict(norm=None, inv_freq=f, interleaved=interleaved)
+    out = api.qk_norm_fwd(q, q.clone(), **kw)
+    grads = api.qk_norm_bwd(q, q.clone(), g, g.clone(), **kw)
+    for got, x in ((out[0], q), (out[1], q), (grads["dq"], g), (grads["dk"], g)):
+        assert torch.equal(got[..., rot:].nan_to_num(7.0), x[..., rot:].nan_to_num(7.0))
+        assert torch.equal(got[..., rot:].isnan(), x[..., rot:].isnan())
+        assert got[..., :rot].isfinite().all()
+
+
 # ------------------------------------------------ gradients through autograd
 
 def _differences(loss, leaves, seed, h=2.0 ** -6):
