@@ -47,6 +47,12 @@ constexpr float kLog2e = 1.4426950408889634f;
 // come out half as far off (8 x 239 tokens: dA 2.3e-6 -> 1.1e-6), at no cost.
 // A step of 0 still has the decay 1.
 constexpr float kLift = 2.3e-8f;
+// A log2 e, -inf taken to the lowest finite value: the steps of 0 that stand
+// for tokens that do not exist leave the state as it is for A = -inf, too.
+__device__ __forceinline__ float rate(float A) {
+  const float a = A * kLog2e;
+  return a < -3.402823466e38f ? -3.402823466e38f : a;  // (NaN stays)
+}
 constexpr int kTile = 32;     // segments are multiples of this many tokens
 constexpr int kCkpt = 8;      // tokens between the backward's saved states, and of its tiles
 
@@ -321,8 +327,8 @@ scan_kernel(Args p) {
     if (cc + k < nc) {
       const long long at = (long long)(c0 + cc + k) * N + nl * 4;
       const float4 v = *reinterpret_cast<const float4*>(p.A + at);
-      a2[k][0] = pack2(v.x * kLog2e, v.y * kLog2e);
-      a2[k][1] = pack2(v.z * kLog2e, v.w * kLog2e);
+      a2[k][0] = pack2(rate(v.x), rate(v.y));
+      a2[k][1] = pack2(rate(v.z), rate(v.w));
       const float* from = nullptr;
       if (MODE != LOCAL) {
         if (p.S > 1)
@@ -439,7 +445,7 @@ chain_kernel(const float* __restrict__ A, const float* __restrict__ h0, float* e
   const long long dn = (long long)D * N;
   const long long b = id / dn, at = id % dn;
   const int d = (int)(at / N);
-  const float a2 = A[at] * kLog2e;
+  const float a2 = rate(A[at]);
   float h = h0 ? h0[id] : 0.f;
   // eight segments' values are loaded before the first is needed
   for (int i0 = 0; i0 < S; i0 += 8) {
@@ -784,8 +790,8 @@ bwd_kernel(BwdArgs q) {
 #pragma unroll
   for (int c = 0; c < 2; ++c) {
     const float4 v = row(p.A, c), w = row(from, c);
-    a2[c][0] = pack2(v.x * kLog2e, v.y * kLog2e);
-    a2[c][1] = pack2(v.z * kLog2e, v.w * kLog2e);
+    a2[c][0] = pack2(rate(v.x), rate(v.y));
+    a2[c][1] = pack2(rate(v.z), rate(v.w));
     e[c][0] = pack2(w.x, w.y);
     e[c][1] = pack2(w.z, w.w);
     dA[c][0] = dA[c][1] = pack2(0.f, 0.f);
@@ -1093,11 +1099,11 @@ step_kernel(Args p, float* __restrict__ S, unsigned tiles) {
     if (p.bias) raw += p.bias[d];
     if (p.Dw) skip = p.Dw[d];
   }
-  const float s = p.softplus ? softplus(raw) : raw, x = s * u, s2 = s * kLog2e;
-  h.x = fmaf(ex2(fmaf(s2, A.x, kLift)), h.x, x * bv.x);
-  h.y = fmaf(ex2(fmaf(s2, A.y, kLift)), h.y, x * bv.y);
-  h.z = fmaf(ex2(fmaf(s2, A.z, kLift)), h.z, x * bv.z);
-  h.w = fmaf(ex2(fmaf(s2, A.w, kLift)), h.w, x * bv.w);
+  const float s = p.softplus ? softplus(raw) : raw, x = s * u;
+  h.x = fmaf(ex2(fmaf(s, rate(A.x), kLift)), h.x, x * bv.x);
+  h.y = fmaf(ex2(fmaf(s, rate(A.y), kLift)), h.y, x * bv.y);
+  h.z = fmaf(ex2(fmaf(s, rate(A.z), kLift)), h.z, x * bv.z);
+  h.w = fmaf(ex2(fmaf(s, rate(A.w), kLift)), h.w, x * bv.w);
   float y = fmaf(cv.w, h.w, fmaf(cv.z, h.z, fmaf(cv.y, h.y, cv.x * h.x)));
 #pragma unroll
   for (int off = LPC / 2; off > 0; off >>= 1) y += __shfl_xor_sync(0xffffffffu, y, off);

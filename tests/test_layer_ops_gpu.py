@@ -303,6 +303,30 @@ def test_ssm_growth_leaves_zeros():
     assert not g["dC"][:, :-1].any()
 
 
+@pytest.mark.parametrize("B,T,D,N,lens", [(2, 37, 70, 16, [37, 5]), (1, 2000, 16, 8, [1990])])
+def test_ssm_states_without_memory(B, T, D, N, lens):
+    """A = -inf (a decay of 0 after every step) is the A whose decay underflows:
+    the places behind the last token keep the state, in both directions."""
+    r = Rand(24)
+    u, dt, z, gy = (r.n(B, T, D) for _ in range(4))
+    A = -0.5 - r.n(D, N).abs()
+    Bm, Cm = r.n(B, T, 1, N), r.n(B, T, 1, N)
+    x = gpu(u, dt, A, Bm, Cm, gy, z)
+    n = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    got = {}
+    for a in (-1e30, -math.inf):
+        x[2][::3, ::2] = a
+        y, h = api.ssm_fwd(*x[:5], z=x[6], lengths=n)
+        state = h.clone()
+        one = api.ssm_step(x[0][:, 0], x[1][:, 0], x[2], x[3][:, 0], x[4][:, 0], state)
+        grads = api.ssm_bwd(*x[:6], z=x[6], lengths=n)
+        got[a] = dict(grads, y=y, h=h, one=one, state=state)
+    for name, v in got[-1e30].items():
+        if v is not None:
+            assert v.isfinite().all(), name
+            assert torch.equal(v, got[-math.inf][name]), name
+
+
 # ------------------------------------------------------- norm and rotation
 
 QK = [  # B, T, Hq, Hk, d, rot, dtype, norm, weight, interleaved, first position, wide
