@@ -547,7 +547,7 @@ static cudaError_t launch_step(const void* x, long long ldx, const float* w, con
 static kla_status check(int B, int T, int D, int W, int dtype, long long ldx) {
   if (B < 1 || T < 0 || D < 1 || W < 1 || !dtype_ok(dtype)) return KLA_ERR_INVALID_ARG;
   if (ldx < D || !size_ok((long long)B * (T > W ? T : W), ldx)) return KLA_ERR_INVALID_ARG;
-  if (T > kMaxTokens || W < 2 || W > 4) return KLA_ERR_UNSUPPORTED;
+  if (T > kMaxTokens || D > kMaxTokens || W < 2 || W > 4) return KLA_ERR_UNSUPPORTED;
   return KLA_OK;
 }
 

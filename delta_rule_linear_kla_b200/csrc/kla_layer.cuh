@@ -53,7 +53,8 @@ inline bool rows_aligned(const void* p, long long n, long long ld, int v, int es
 }
 inline bool misplaced(const void* p, int es) { return (uintptr_t)p % (uintptr_t)es != 0; }
 
-// Longest sequence: token indices and their roundings up stay inside an int.
+// Longest sequence, and most channels of one: their indices and roundings up
+// to blocks stay inside an int.
 constexpr int kMaxTokens = 1 << 30;
 
 inline bool dtype_ok(int dtype) { return dtype == KLA_BF16 || dtype == KLA_FP32; }

@@ -1297,7 +1297,8 @@ static kla_status check(int B, int T, int D, int G, int N, int dtype) {
       !size_ok((long long)B * D, (long long)N * (T / kCkpt + 1)) ||
       !size_ok((long long)B * (T > 0 ? T : 1), 2LL * G * N * 4))
     return KLA_ERR_INVALID_ARG;
-  if (T > kMaxTokens || (N != 8 && N != 16 && N != 32 && N != 64)) return KLA_ERR_UNSUPPORTED;
+  if (T > kMaxTokens || D > kMaxTokens || (N != 8 && N != 16 && N != 32 && N != 64))
+    return KLA_ERR_UNSUPPORTED;
   return KLA_OK;
 }
 

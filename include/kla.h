@@ -430,7 +430,7 @@ KLA_API kla_status kla_gdn_recurrent_bwd(const void *q, const void *k, const voi
  *     min(max(lengths[b], 0), T) tokens.  The tokens behind are not read,
  *     whatever they hold; their outputs and gradients are written as zeros,
  *     and the final state is the one after the last token that exists.
- *   * T <= 2^30.  Sums over tokens and channels are taken in a fixed order (no
+ *   * T and D <= 2^30.  Sums over tokens and channels are taken in a fixed order (no
  *     atomics): the same call gives the same bits.
  *
  * Short causal depthwise convolution (arXiv 2312.00752, section 3.4, puts it

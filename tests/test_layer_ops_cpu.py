@@ -138,6 +138,7 @@ def test_conv_refusals(lib):
     assert fwd(B=2**31 - 1, T=2**30, D=2**20, ldx=2**20) == INVALID  # 2^81 elements
     assert fwd(W=1) == fwd(W=5) == UNSUPPORTED
     assert fwd(B=1, T=2**30 + 1, D=1, ldx=1) == UNSUPPORTED
+    assert fwd(B=1, T=1, D=2**31 - 1, ldx=2**31 - 1) == UNSUPPORTED
     # a written buffer between the first and the last row of a wide matrix
     assert fwd(ldx=1 << 20, y=A + (1 << 21)) == INVALID
     need = lib.kla_conv_bwd_workspace_size(2, 16, 64, 4)
@@ -189,6 +190,7 @@ def test_ssm_refusals(lib):
         0, None)
     assert step(S=None) == step(y=None) == step(S=A) == step(y=6 * A) == INVALID
     assert step(N=24) == UNSUPPORTED
+    assert lib.kla_ssm_bwd_workspace_size(1, 1, 2**30 + 1, 1, 16) == 0   # too many channels
 
 
 def test_qk_norm_refusals(lib):
