@@ -1091,8 +1091,9 @@ step_kernel(Args p, float* __restrict__ S, unsigned tiles) {
     const int g = d / (p.D / p.G);
     h = *reinterpret_cast<const float4*>(at);
     A = *reinterpret_cast<const float4*>(p.A + (long long)d * N + nl * 4);
-    bv = ld4((const T*)p.Bm + b * p.ldb + g * N + nl * 4, 4, p.vb);
-    cv = ld4((const T*)p.Cm + b * p.ldc + g * N + nl * 4, 4, p.vc);
+    const long long gn = (long long)g * N + nl * 4;
+    bv = ld4((const T*)p.Bm + b * p.ldb + gn, 4, p.vb);
+    cv = ld4((const T*)p.Cm + b * p.ldc + gn, 4, p.vc);
     raw = IO<T>::ld((const T*)p.dt + b * p.lddt + d);
     u = IO<T>::ld((const T*)p.u + b * p.ldu + d);
     if (p.z) z = IO<T>::ld((const T*)p.z + b * p.ldz + d);
