@@ -352,6 +352,9 @@ qk_kernel(Args p, long long ntiles) {
         x[i].get(v);
         if (p.norm) {
           r = rsqrt_ftz(fmaf(row_dot<LPR>(v, v), inv_m, p.eps));
+          // a place without a row holds zeros: without an eps they would give
+          // 0 / 0 to the weights' sums
+          if (BWD && !live) r = 0.f;
 #pragma unroll
           for (int e = 0; e < 4; ++e) v[e] = mul2(v[e], both(r));
         }

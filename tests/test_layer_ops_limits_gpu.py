@@ -3,6 +3,8 @@ import pytest
 import torch
 
 from delta_rule_linear_kla_b200 import api
+from oracle import layer_ops as ref
+from test_layer_ops_gpu import Rand, check, gpu
 
 pytestmark = pytest.mark.gpu
 
@@ -27,3 +29,30 @@ def test_ssm_step_groups_past_32_bits():
     y = api.ssm_step(u, dt, A, Bm, Cm, S)
     want = api.ssm_step(cut[0], cut[1], A[-tail:].contiguous(), cut[2], cut[3], cut[4])
     assert torch.equal(y[:, -tail:], want) and torch.equal(S[:, -tail:], cut[4])
+
+
+NOEPS = [  # B, T, Hq, Hk, d: heads or tokens that do not fill a block
+    (1, 7, 5, 1, 128), (2, 5, 1, 1, 64), (1, 1, 3, 2, 80), (3, 41, 2, 0, 8), (1, 301, 17, 3, 32),
+]
+
+
+@pytest.mark.parametrize("eps", [0.0, 1e-40])  # 1e-40: below fp32's normal range
+@pytest.mark.parametrize("norm", ["l2", "rms"])
+@pytest.mark.parametrize("case", NOEPS, ids=str)
+def test_qk_norm_without_eps(case, norm, eps):
+    """No eps: the row places of a block that hold no row add nothing to the
+    weights' gradients (a row of zeros there would be 0 / 0).  Bars as for the
+    other norms: c = 64, 128 backward, and a unit for every 16 rows of dw."""
+    B, T, Hq, Hk, d = case
+    r = Rand(71)
+    q, k, gq, gk = (r.n(B, T, h, d) for h in (Hq, Hk, Hq, Hk))
+    w = r.n(d)
+    qg, kg, gqg, gkg, wg = gpu(q, k, gq, gk, w)
+    kw = dict(norm=norm, eps=eps)
+    out = api.qk_norm_fwd(qg, kg, wq=wg, wk=wg, **kw)
+    got = api.qk_norm_bwd(qg, kg, gqg, gkg, wq=wg, wk=wg, **kw)
+    for i, (n, x, g) in enumerate((("q", q, gq), ("k", k, gk))):
+        check(out[i], ref.head_norm(x, w, **kw), 64, n)
+        want = ref.head_norm_bwd(x, g, w, **kw)
+        check(got["d" + n], want["dx"], 128, "d" + n)
+        check(got["dw" + n], want["dw"], 128 + x[..., 0].numel() / 16, "dw" + n)
