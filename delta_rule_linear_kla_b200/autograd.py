@@ -27,6 +27,20 @@ from torch.autograd.function import once_differentiable
 from . import api
 
 
+def _given(g, dtype):
+    """A gradient as the library takes it (None stays None): of this type,
+    contiguous and 16-byte aligned.  Autograd's may be a view that starts at
+    any element of another tensor."""
+    if g is None:
+        return None
+    g = g.to(dtype).contiguous()
+    return g.clone() if g.data_ptr() % 16 else g
+
+
+def _or_zeros(g, like):
+    return like.new_zeros(like.shape) if g is None else _given(g, like.dtype)
+
+
 class _KLAPrefill(torch.autograd.Function):
     @staticmethod
     def forward(ctx, q, k, v, g, eta, h0, eps):
@@ -40,10 +54,8 @@ class _KLAPrefill(torch.autograd.Function):
         q, k, v, g, eta, h0 = ctx.saved_tensors
         if grad_o is None:
             grad_o = torch.zeros_like(q[..., :v.shape[-1]])
-        grad_o = grad_o.to(q.dtype).contiguous()
-        if grad_hT is not None:
-            grad_hT = grad_hT.float().contiguous()
-        r = api.chunk_bwd(q, k, v, g, eta, grad_o, ctx.eps, h0, grad_hT,
+        r = api.chunk_bwd(q, k, v, g, eta, _given(grad_o, q.dtype), ctx.eps, h0,
+                          _given(grad_hT, torch.float32),
                           need_h0=h0 is not None and ctx.needs_input_grad[5])
         dh0 = r["dh0"] if h0 is not None else None
         return (r["dq"].to(q.dtype), r["dk"].to(k.dtype), r["dv"].to(v.dtype), r["dg"],
@@ -53,11 +65,6 @@ class _KLAPrefill(torch.autograd.Function):
 def kla_prefill(q, k, v, g, eta, eps: float = 1e-6, h0=None):
     """Differentiable KLA prefill: returns (o, hT)."""
     return _KLAPrefill.apply(q, k, v, g, eta, h0, eps)
-
-
-def _given(g, like):
-    """A gradient as the library wants it: zeros where autograd has none."""
-    return like.new_zeros(like.shape) if g is None else g.to(like.dtype).contiguous()
 
 
 class _KLAConv(torch.autograd.Function):
@@ -73,11 +80,7 @@ class _KLAConv(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, grad_y, grad_sT):
         x, w, bias, s0, lengths = ctx.saved_tensors
-        if grad_y is None:
-            grad_y = x.new_zeros(x.shape)
-        if grad_sT is not None:
-            grad_sT = grad_sT.to(x.dtype).contiguous()
-        r = api.conv_bwd(x, w, grad_y.to(x.dtype).contiguous(), bias, s0, grad_sT,
+        r = api.conv_bwd(x, w, _or_zeros(grad_y, x), bias, s0, _given(grad_sT, x.dtype),
                          silu=ctx.silu, lengths=lengths,
                          need_s0=s0 is not None and ctx.needs_input_grad[3])
         return r["dx"], r["dw"], r["dbias"], r["ds0"], None, None
@@ -103,12 +106,8 @@ class _KLASSM(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, grad_y, grad_hT):
         u, dt, A, Bm, Cm, D, z, dt_bias, h0, lengths = ctx.saved_tensors
-        if grad_y is None:
-            grad_y = u.new_zeros(u.shape)
-        if grad_hT is not None:
-            grad_hT = grad_hT.float().contiguous()
-        r = api.ssm_bwd(u, dt, A, Bm, Cm, grad_y.to(u.dtype).contiguous(), D, z, dt_bias, h0,
-                        grad_hT, softplus=ctx.softplus, lengths=lengths,
+        r = api.ssm_bwd(u, dt, A, Bm, Cm, _or_zeros(grad_y, u), D, z, dt_bias, h0,
+                        _given(grad_hT, torch.float32), softplus=ctx.softplus, lengths=lengths,
                         need_h0=h0 is not None and ctx.needs_input_grad[8])
         return (r["du"], r["ddt"], r["dA"], r["dB"], r["dC"], r["dD"], r["dz"], r["ddt_bias"],
                 r["dh0"], None, None)
@@ -135,7 +134,7 @@ class _KLAQKNorm(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, gq, gk):
         q, k, wq, wk, positions, inv_freq = ctx.saved_tensors
-        r = api.qk_norm_bwd(q, k, _given(gq, q), _given(gk, k), wq=wq, wk=wk,
+        r = api.qk_norm_bwd(q, k, _or_zeros(gq, q), _or_zeros(gk, k), wq=wq, wk=wk,
                             positions=positions, inv_freq=inv_freq, **ctx.kw)
         return r["dq"], r["dk"], r["dwq"], r["dwk"], None, None, None
 

@@ -2,9 +2,10 @@
 import pytest
 import torch
 
+import delta_rule_linear_kla_b200 as K
 from delta_rule_linear_kla_b200 import api
 from oracle import layer_ops as ref
-from test_layer_ops_gpu import Rand, check, gpu
+from test_layer_ops_gpu import DT, Rand, check, gpu
 
 pytestmark = pytest.mark.gpu
 
@@ -56,3 +57,46 @@ def test_qk_norm_without_eps(case, norm, eps):
         want = ref.head_norm_bwd(x, g, w, **kw)
         check(got["d" + n], want["dx"], 128, "d" + n)
         check(got["dw" + n], want["dw"], 128 + x[..., 0].numel() / 16, "dw" + n)
+
+
+def _given_as(y, other, tail):
+    """Gradients of `tail` for y whole and for y behind `other` in one tensor:
+    the gradient then is a contiguous view that starts at any element."""
+    c = torch.arange(y.numel(), device=y.device).to(y.dtype).reshape(y.shape) / y.numel() - 0.5
+    whole = torch.autograd.grad(y, tail, c, retain_graph=True)
+    flat = torch.cat([other.flatten(), y.flatten()])
+    behind = torch.autograd.grad(flat, tail, torch.cat([torch.zeros_like(other).flatten(),
+                                                        c.flatten()]), retain_graph=True)
+    return zip(whole, behind)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp32"])
+def test_gradients_that_start_at_any_element(dt):
+    """Autograd hands the backward pass of a concatenation's part a view: the
+    same bits as for a gradient of its own memory."""
+    r = Rand(72)
+    t = DT[dt]
+    leaf = lambda *s: r.n(*s, dt=t).cuda().requires_grad_(True)  # noqa: E731
+    odd = torch.zeros(5, device="cuda", dtype=t)
+    odd32 = torch.zeros(5, device="cuda")
+    D, N = 3, 8
+    x, w = leaf(1, 7, D), r.n(D, 4).cuda().requires_grad_(True)
+    y, sT = K.kla_conv(x, w)
+    bc, A = leaf(1, 7, 1, N), (-torch.rand(D, N).cuda()).requires_grad_(True)
+    o, hT = K.kla_ssm(x, x, A, bc, bc)
+    q = leaf(1, 7, 2, 8)
+    nq, nk = K.kla_qk_norm(q, q)
+    for out, other, to in ((y, odd, [x, w]), (sT, odd, [x]), (o, odd, [x, A, bc]),
+                           (hT, odd32, [x, A, bc]), (nq, odd, [q]), (nk, odd, [q])):
+        for a, b in _given_as(out, other, to):
+            assert torch.equal(a, b) and a.abs().sum() > 0
+
+
+def test_prefill_gradients_that_start_at_any_element():
+    r = Rand(73)
+    q, k, v = (r.n(1, 65, 1, 64, dt=torch.bfloat16).cuda().requires_grad_(True) for _ in range(3))
+    g, eta = -0.1 * torch.rand(1, 65, 1, device="cuda"), torch.rand(1, 65, 1, device="cuda")
+    o, hT = K.kla_prefill(q, k, v, g, eta)
+    for out, to in ((o, [q, k, v]), (hT, [k, v])):
+        for a, b in _given_as(out, torch.zeros(5, device="cuda", dtype=out.dtype), to):
+            assert torch.equal(a, b) and a.abs().sum() > 0
