@@ -16,7 +16,7 @@
 // thread stays with one token and walks through some of its heads, so that
 // cosines and sines are formed once a token and held in registers, and loads
 // the rows of several heads before it needs the first.  Angles are formed and reduced to [-pi, pi] in fp64 (a position of
-// 1e6 leaves 24-bit angles 0.06 off), their cosine and sine in fp32 (2^-21); norms
+// 1e6 leaves 24-bit angles 0.06 off), their cosine and sine in fp32; norms
 // and products are fp32, and only the results are rounded, once.
 // Measured: 8 x 4096 tokens of 8 + 8 heads of 128, half of each turned, bf16:
 // 48 us, 5.5 TB/s of the 6.45 that a copy reaches.  Backward, 4 x 8192 tokens of
@@ -95,7 +95,11 @@ __device__ __forceinline__ void store8(float* p, const f32x2 (&f)[4]) {
 // SMEM through shared memory (any even rot).
 enum Reach { NONE = 0, PAIR = 1, LANE = 2, SMEM = 3 };
 
-// Cosines and sines of the block's nt tokens, [token][pair], times scale.
+// Cosines and sines of the block's nt tokens, [token][pair], times scale.  fp32
+// rows get them within 2.6 units of 2^-24 (the angle's rounding, as a multiple
+// of pi in [-1, 1], and 1 ulp); bf16 rows, whose results are rounded by up to 2^-8,
+// within 2^-21 by the fast form.
+template <typename T>
 __device__ __forceinline__ void make_angles(const Args& p, long long tok0, int nt, float* s_cos,
                                             float* s_sin) {
   const unsigned np = p.rot / 2;
@@ -108,9 +112,12 @@ __device__ __forceinline__ void make_angles(const Args& p, long long tok0, int n
     const int at = p.pos ? p.pos[(b0 + more) * p.pos_stride + t] : p.pos0 + (int)t;
     const double ang = (double)at * (double)p.inv_freq[j];
     const double turns = rint(ang * 0.15915494309189535);  // 1 / 2 pi
-    const float r = (float)fma(-turns, 6.283185307179586, ang);
+    const double r = fma(-turns, 6.283185307179586, ang);  // in [-pi, pi]
     float s, c;
-    __sincosf(r, &s, &c);  // within 2^-21 on [-pi, pi]
+    if constexpr (sizeof(T) == 4)
+      sincospif((float)(r * 0.3183098861837907), &s, &c);
+    else
+      __sincosf((float)r, &s, &c);
     s_cos[i] = c * p.scale;
     s_sin[i] = s * p.scale;
   }
@@ -319,7 +326,7 @@ qk_kernel(Args p, long long ntiles) {
     Turn<REACH> turn;
     if constexpr (REACH != NONE) {
       if (tile != blockIdx.x) __syncthreads();  // the last tile's angles are read
-      make_angles(p, tok0, nt, s_cos, s_sin);
+      make_angles<T>(p, tok0, nt, s_cos, s_sin);
       __syncthreads();
       const int mine_at = tt < nt ? tt * (p.rot / 2) : 0;
       turn.load(p, c, s_cos + mine_at, s_sin + mine_at);

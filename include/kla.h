@@ -532,7 +532,9 @@ KLA_API kla_status kla_ssm_step(const void *u, const void *dt, const float *A, c
  *   q [B][T][Hq][d] dtype [ldq], k [B][T][Hk][d] dtype [ldk] (Hq or Hk may be 0)
  *   wq, wk [d] fp32, nullable = 1;  inv_freq [rot/2] fp32 (rot = 0: none)
  *   positions: int32 [B][T] with rows pos_stride apart (0: one row for all
- *   sequences); NULL = pos0 + t, at most 2^31 - 1.  Angles are formed in fp64.
+ *   sequences); NULL = pos0 + t, at most 2^31 - 1.  Angles are formed in fp64,
+ *   their cosine and sine in fp32: within 3 * 2^-24 for KLA_FP32, 2^-21 for
+ *   KLA_BF16.
  *   oq, ok: contiguous, dtype, written.
  * d a multiple of 8, at most 256; ldq and ldk multiples of 16 bytes (else
  * KLA_ERR_UNSUPPORTED); rot even, at most d.  Inverse frequencies stretched

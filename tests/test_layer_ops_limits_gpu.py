@@ -5,7 +5,7 @@ import torch
 import delta_rule_linear_kla_b200 as K
 from delta_rule_linear_kla_b200 import api
 from oracle import layer_ops as ref
-from test_layer_ops_gpu import DT, Rand, check, gpu
+from test_layer_ops_gpu import DT, Rand, U, check, gpu
 
 pytestmark = pytest.mark.gpu
 
@@ -100,3 +100,22 @@ def test_prefill_gradients_that_start_at_any_element():
     for out, to in ((o, [q, k, v]), (hT, [k, v])):
         for a, b in _given_as(out, torch.zeros(5, device="cuda", dtype=out.dtype), to):
             assert torch.equal(a, b) and a.abs().sum() > 0
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_rotation_of_fp32_rows(interleaved):
+    """The cosine and sine that fp32 rows are turned by, read off rows of one 1
+    and zeros, over 10^5 angles up to 10^6 radians.  In units of 2^-24: the
+    angle, a multiple of pi in [-1, 1], rounded to fp32 turns by pi 2^-25 at
+    most (1.6); sine and cosine within 1 ulp of values up to 1 (1), and the
+    products with 1 and 0 add nothing: 2.6, and 0.1 for what is of second
+    order and the fp64 angle (10^6 2^-53)."""
+    T, d = 8000, 32
+    f = torch.linspace(1e-3, 1.0, d // 2)
+    pos = (torch.arange(T) * 125).int()
+    x = torch.zeros(1, T, 1, d)
+    x[..., (slice(0, d, 2) if interleaved else slice(0, d // 2))] = 1.0
+    kw = dict(norm=None, interleaved=interleaved)
+    got, _ = api.qk_norm_fwd(x.cuda(), x.cuda(), inv_freq=f.cuda(), positions=pos.cuda(), **kw)
+    want, _ = ref.head_norm(x, None, pos[None], f, **kw)
+    assert float((got.double().cpu() - want).abs().max()) <= 2.7 * U
