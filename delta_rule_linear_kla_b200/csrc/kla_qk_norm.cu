@@ -230,11 +230,6 @@ struct Turn<NONE> {
   __device__ __forceinline__ void reverse() {}
 };
 
-__device__ __forceinline__ float rsqrt_ftz(float x) {
-  float y;
-  asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 // sum of a lane's eight products, then of the row's lanes
 template <int LPR>
 __device__ __forceinline__ float row_dot(const f32x2 (&a)[4], const f32x2 (&b)[4]) {
@@ -358,7 +353,8 @@ qk_kernel(Args p, long long ntiles) {
         float r = 1.f;
         x[i].get(v);
         if (p.norm) {
-          r = rsqrt_ftz(fmaf(row_dot<LPR>(v, v), inv_m, p.eps));
+          // (not the flushing form: without an eps the sum may be subnormal)
+          r = rsqrtf(fmaf(row_dot<LPR>(v, v), inv_m, p.eps));
           // a place without a row holds zeros: without an eps they would give
           // 0 / 0 to the weights' sums
           if (BWD && !live) r = 0.f;

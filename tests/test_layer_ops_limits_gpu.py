@@ -119,3 +119,24 @@ def test_rotation_of_fp32_rows(interleaved):
     got, _ = api.qk_norm_fwd(x.cuda(), x.cuda(), inv_freq=f.cuda(), positions=pos.cuda(), **kw)
     want, _ = ref.head_norm(x, None, pos[None], f, **kw)
     assert float((got.double().cpu() - want).abs().max()) <= 2.7 * U
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp32"])
+def test_qk_norm_of_tiny_rows_without_eps(dt):
+    """Rows of entries near 5e-21 without an eps: their squares and the sum of
+    them (3e-39) lie below fp32's normal range, where a square is off by 2^-150
+    at most and a sum of 128 by 2^-142 in all, 2^-14 of the sum; half of that
+    in the norm, 2^-15 of the result.  Backward twice that, and for dw."""
+    r = Rand(74)
+    d = 128
+    q = ((r.n(2, 9, 2, d).sign() * (4e-21 + 2e-21 * torch.rand(2, 9, 2, d)))).to(DT[dt])
+    g, w = r.n(2, 9, 2, d, dt=DT[dt]), r.n(d)
+    qg, gg, wg = gpu(q, g, w)
+    kw = dict(norm="l2", eps=0.0)
+    out, _ = api.qk_norm_fwd(qg, qg.clone(), wq=wg, **kw)
+    got = api.qk_norm_bwd(qg, qg.clone(), gg, gg.clone(), wq=wg, **kw)
+    c = 2.0 ** 9  # 2^-15 in units of 2^-24
+    check(out, ref.head_norm(q, w, **kw), c, "out")
+    want = ref.head_norm_bwd(q, g, w, **kw)
+    check(got["dq"], want["dx"], 2 * c, "dq")
+    check(got["dwq"], want["dw"], 2 * c, "dwq")
