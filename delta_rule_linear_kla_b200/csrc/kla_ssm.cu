@@ -53,6 +53,13 @@ __device__ __forceinline__ float rate(float A) {
   const float a = A * kLog2e;
   return a < -3.402823466e38f ? -3.402823466e38f : a;  // (NaN stays)
 }
+// 2^x h for the decay 2^x of many tokens, as 2^{x/2} h 2^{x/2}: the factor alone
+// may leave fp32's range where the product does not.  A state of 0 stays 0
+// under any growth.
+__device__ __forceinline__ float carried(float x, float h) {
+  const float f = ex2(0.5f * x);
+  return h == 0.f ? 0.f : f * h * f;
+}
 constexpr int kTile = 32;     // segments are multiples of this many tokens
 constexpr int kCkpt = 8;      // tokens between the backward's saved states, and of its tiles
 
@@ -463,8 +470,7 @@ chain_kernel(const float* __restrict__ A, const float* __restrict__ h0, float* e
     for (int j = 0; j < 8; ++j) {
       const int i = i0 + j, s = REV ? S - 1 - i : i;
       if (i < S) ends[(b * S + s) * dn + at] = h;
-      // (a state of 0 stays 0 under a growth past fp32's range)
-      h = h == 0.f ? own[j] : fmaf(ex2(a2 * sum[j]), h, own[j]);
+      h = carried(a2 * sum[j], h) + own[j];
     }
   }
 }
@@ -853,13 +859,9 @@ bwd_kernel(BwdArgs q) {
         if (q.fS > 1) {  // saved from a zero start: add what the segment's start left
           const float4 w = reorder(v[(2 + c) * CW * 32], ord);
           const f32x2 s2 = c ? pack2(s.y, s.y) : pack2(s.x, s.x);
-          const float2 g0 = unpack2(ex2_2(mul2(s2, a2[c][0])));
-          const float2 g1 = unpack2(ex2_2(mul2(s2, a2[c][1])));
-          // (a start of 0 leaves 0 under a growth past fp32's range)
-          h0[c][0] = add2(h0[c][0], pack2(w.x == 0.f ? 0.f : g0.x * w.x,
-                                          w.y == 0.f ? 0.f : g0.y * w.y));
-          h0[c][1] = add2(h0[c][1], pack2(w.z == 0.f ? 0.f : g1.x * w.z,
-                                          w.w == 0.f ? 0.f : g1.y * w.w));
+          const float2 x0 = unpack2(mul2(s2, a2[c][0])), x1 = unpack2(mul2(s2, a2[c][1]));
+          h0[c][0] = add2(h0[c][0], pack2(carried(x0.x, w.x), carried(x0.y, w.y)));
+          h0[c][1] = add2(h0[c][1], pack2(carried(x1.x, w.z), carried(x1.y, w.w)));
         }
       }
     }

@@ -140,3 +140,35 @@ def test_qk_norm_of_tiny_rows_without_eps(dt):
     want = ref.head_norm_bwd(q, g, w, **kw)
     check(got["dq"], want["dx"], 2 * c, "dq")
     check(got["dwq"], want["dw"], 2 * c, "dwq")
+
+
+@pytest.mark.parametrize("late", [False, True])  # the steps in the first or the second segment
+@pytest.mark.parametrize("sign,start", [(1.0, 1e-20), (-1.0, 1e30)])
+def test_ssm_segment_factors_past_fp32(sign, start, late):
+    """A segment whose states grow (or decay) by e^96 = 2^138 as a whole, from
+    a start that keeps every state inside fp32, forward and backward.  Bars of
+    the other scans: c = 64 + (7 + 3 X) T, X = 0.75."""
+    B, T, D, N = 1, 256, 16, 8
+    assert api.ssm_fwd_workspace_size(B, T, D, 1, N) > 0  # cut into two segments
+    r = Rand(75)
+    dt = torch.zeros(B, T, D)
+    dt[:, 128:] += 0.75 * late
+    dt[:, :128] += 0.75 * (not late)
+    u, A = torch.zeros(B, T, D), torch.full((D, N), sign)
+    Bm, Cm = r.n(B, T, 1, N), r.n(B, T, 1, N)
+    h0 = start * (1 + torch.rand(B, D, N))
+    # the adjoint state makes the same way from the other end
+    gy, gh = torch.zeros(B, T, D), (1e-12 if sign > 0 else 1.0) * (1 + torch.rand(B, D, N))
+    c = 64 + (7 + 3 * 0.75) * T
+    a = dict(u=u, dt=dt, A=A, Bm=Bm, Cm=Cm, h0=h0)
+    x = {k: v.cuda() for k, v in a.items()}
+    y, h = api.ssm_fwd(**x, softplus=False)
+    want = ref.ssm(**a, softplus=False)
+    check(y, want["y"], c, "y")
+    check(h, want["hT"], c, "hT")
+    got = api.ssm_bwd(x["u"], x["dt"], x["A"], x["Bm"], x["Cm"], gy.cuda(), h0=x["h0"],
+                      grad_hT=gh.cuda(), softplus=False)
+    want = ref.ssm_bwd(u, dt, A, Bm, Cm, gy, h0=h0, ghT=gh, softplus=False)
+    for k, v in got.items():
+        if v is not None:
+            check(v, want[k], 2 * c + 128, k)
