@@ -40,13 +40,18 @@ namespace ssm {
 using namespace layer;
 
 constexpr float kLog2e = 1.4426950408889634f;
-// ex2.approx is low on average: measured over [-4, 0] by 0.6e-8 next to 0, 2.4e-8
-// from -0.5 to -0.005 and 5e-8 below -0.5 (relative; a product of many decays
-// adds that up).  Added to every decay's exponent, in the multiply-add that
-// forms it, this takes 1.6e-8 of it away: states and gradients of long memories
-// come out half as far off (8 x 239 tokens: dA 2.3e-6 -> 1.1e-6), at no cost.
-// A step of 0 still has the decay 1.
-constexpr float kLift = 2.3e-8f;
+// ex2.approx is low on average, and a product of many decays adds that up.
+// Measured (relative): by 0.5e-8 for exponents from -0.003 to -0.0001, 2.4e-8 from
+// -0.05 to -0.005, 1.4 to 2e-8 to -0.5, 5e-8 below -1.  A token's decays get a
+// constant added to their exponent, in the multiply-add that forms it, that takes
+// 0.6e-8 away where a thread's exponents are small and 1.6e-8 elsewhere.  One
+// constant a thread and segment, by the first token of the first tile that it
+// comes to: one for all (2.3e-8) leaves memories of 300 tokens and more farther
+// off than none (8 x 1024 tokens: states 4.2e-6 from the definition, 3.5e-6 with
+// none, 2.9e-6 so), one a tile takes longer (backward 580 us, 573 so, 570 with one
+// for all).  8 x 239 tokens: dA 2.7e-6 with none, 1.1e-6 so.  A step of 0 still
+// has the decay 1.  (The decays of whole segments go without: carried().)
+__device__ __forceinline__ float lift(float x) { return x > -4e-3f ? 0.9e-8f : 2.3e-8f; }
 // A log2 e, -inf taken to the lowest finite value: the steps of 0 that stand
 // for tokens that do not exist leave the state as it is for A = -inf, too.
 __device__ __forceinline__ float rate(float A) {
@@ -359,6 +364,7 @@ scan_kernel(Args p) {
             make_float4(u.x, u.y, v.x, v.y);
       }
   };
+  f32x2 up;  // what lifts the exponents of the tokens' decays
   auto scan = [&](int k) {
     const float* sd = s_d + (k & 1) * TK * CH + cc;
     const float* sx = s_x + (k & 1) * TK * CH + cc;
@@ -400,8 +406,8 @@ scan_kernel(Args p) {
 #pragma unroll
         for (int c = 0; c < CPT; ++c) {
           const f32x2 d2 = both(d[c]), w2 = both(x[c]);
-          const f32x2 e0 = ex2_2(fma2(d2, a2[c][0], both(kLift)));
-          const f32x2 e1 = ex2_2(fma2(d2, a2[c][1], both(kLift)));
+          const f32x2 e0 = ex2_2(fma2(d2, a2[c][0], up));
+          const f32x2 e1 = ex2_2(fma2(d2, a2[c][1], up));
           if (REV) {
             h[c][0] = mul2(e0, fma2(w2, cv[0], h[c][0]));
             h[c][1] = mul2(e1, fma2(w2, cv[1], h[c][1]));
@@ -428,6 +434,8 @@ scan_kernel(Args p) {
     }
   };
   __syncthreads();
+  // (without a tile: whatever lies there, for nothing; a guard costs 1 %)
+  up = both(lift(s_d[(first & 1) * TK * CH + cc] * unpack2(a2[0][0]).x));
   for (int i = 0; i < ntile; ++i) {
     scan(first + dir * i);
     __syncthreads();
@@ -836,6 +844,7 @@ bwd_kernel(BwdArgs q) {
   };
   if (ntile > 0) fetch(ntile - 1);
   __syncthreads();
+  const f32x2 up = both(lift(smem[((ntile - 1) & 1) * Sh::BUF + cc] * unpack2(a2[0][0]).x));
   for (int k = ntile - 1; k >= 0; --k) {
     float* buf = smem + (k & 1) * Sh::BUF;
     const float* sd = buf + cc;
@@ -876,8 +885,8 @@ bwd_kernel(BwdArgs q) {
       for (int c = 0; c < 2; ++c) {
         const f32x2 d2 = c ? pack2(d.y, d.y) : pack2(d.x, d.x);
         const f32x2 x2 = c ? pack2(x.y, x.y) : pack2(x.x, x.x);
-        a[c][0] = ex2_2(fma2(d2, a2[c][0], both(kLift)));
-        a[c][1] = ex2_2(fma2(d2, a2[c][1], both(kLift)));
+        a[c][0] = ex2_2(fma2(d2, a2[c][0], up));
+        a[c][1] = ex2_2(fma2(d2, a2[c][1], up));
         h[c][0] = fma2(a[c][0], h[c][0], mul2(x2, bv.x));
         h[c][1] = fma2(a[c][1], h[c][1], mul2(x2, bv.y));
       }
@@ -1103,10 +1112,11 @@ step_kernel(Args p, float* __restrict__ S, unsigned tiles) {
     if (p.Dw) skip = p.Dw[d];
   }
   const float s = p.softplus ? softplus(raw) : raw, x = s * u;
-  h.x = fmaf(ex2(fmaf(s, rate(A.x), kLift)), h.x, x * bv.x);
-  h.y = fmaf(ex2(fmaf(s, rate(A.y), kLift)), h.y, x * bv.y);
-  h.z = fmaf(ex2(fmaf(s, rate(A.z), kLift)), h.z, x * bv.z);
-  h.w = fmaf(ex2(fmaf(s, rate(A.w), kLift)), h.w, x * bv.w);
+  const float up = lift(s * rate(A.x));
+  h.x = fmaf(ex2(fmaf(s, rate(A.x), up)), h.x, x * bv.x);
+  h.y = fmaf(ex2(fmaf(s, rate(A.y), up)), h.y, x * bv.y);
+  h.z = fmaf(ex2(fmaf(s, rate(A.z), up)), h.z, x * bv.z);
+  h.w = fmaf(ex2(fmaf(s, rate(A.w), up)), h.w, x * bv.w);
   float y = fmaf(cv.w, h.w, fmaf(cv.z, h.z, fmaf(cv.y, h.y, cv.x * h.x)));
 #pragma unroll
   for (int off = LPC / 2; off > 0; off >>= 1) y += __shfl_xor_sync(0xffffffffu, y, off);
