@@ -497,18 +497,34 @@ static long long bwd_parts(int B, int T, int D, int V) {
   return (long long)B * ((T + kBY * L - 1) / (kBY * L));
 }
 
+// Sequences of one launch with this many threads each: kernels count their
+// threads in 32 bits, and single channels of short prompts or tokens can be more
+// (2^32 of them take 17 GB).  A sequence alone is not: D <= 2^30, and four walks
+// of 32 tokens of that many channels do not fit the memory.
+static int launch_batch(int B, long long threads) {
+  const long long most = 0xffffff00LL / threads;
+  return (int)(B < most ? B : most);
+}
+
 template <typename T, int V, int W>
 static cudaError_t launch_fwd(const void* x, long long ldx, const float* w, const float* bias,
                               const void* s0, const int* lengths, void* y, void* sT, int B,
                               int Tn, int D, bool silu, cudaStream_t st) {
   const int CG = D / V, L = fwd_walk(B, Tn, CG), NB = (Tn + L - 1) / L;
-  const long long total = (long long)B * NB * CG, blocks = (total + kFT - 1) / kFT;
-  // (more threads than 32 bits count would need more memory than there is)
-  if (total > 0xffffff00LL) return cudaErrorInvalidValue;
+  const int per = launch_batch(B, (long long)NB * CG);
+  if (per < 1) return cudaErrorInvalidValue;
   auto k = silu ? conv_fwd_kernel<T, V, W, true> : conv_fwd_kernel<T, V, W, false>;
-  k<<<(unsigned)blocks, kFT, 0, st>>>((const T*)x, ldx, w, bias, (const T*)s0, lengths, (T*)y,
-                                      (T*)sT, Tn, D, CG, NB, L, (unsigned)total);
-  return cudaGetLastError();
+  for (int b = 0; b < B; b += per) {
+    const long long rows = (long long)b * Tn, st_at = (long long)b * (W - 1) * D;
+    const unsigned total = (unsigned)((long long)(B - b < per ? B - b : per) * NB * CG);
+    k<<<(total - 1) / kFT + 1, kFT, 0, st>>>(
+        (const T*)x + rows * ldx, ldx, w, bias, s0 ? (const T*)s0 + st_at : nullptr,
+        lengths ? lengths + b : nullptr, (T*)y + rows * D, sT ? (T*)sT + st_at : nullptr, Tn, D,
+        CG, NB, L, total);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess || B - b <= per) return e;
+  }
+  return cudaSuccess;
 }
 
 template <typename T, int V, int W>
@@ -535,12 +551,17 @@ template <typename T, int V, int W>
 static cudaError_t launch_step(const void* x, long long ldx, const float* w, const float* bias,
                                void* s, void* y, int B, int D, bool silu, cudaStream_t st) {
   const int CG = D / V;
-  const long long total = (long long)B * CG, blocks = (total + 127) / 128;
-  if (total > 0xffffff00LL) return cudaErrorInvalidValue;
+  const int per = launch_batch(B, CG);
   auto k = silu ? conv_step_kernel<T, V, W, true> : conv_step_kernel<T, V, W, false>;
-  k<<<(unsigned)blocks, 128, 0, st>>>((const T*)x, ldx, w, bias, (T*)s, (T*)y, D, CG,
-                                      (unsigned)total);
-  return cudaGetLastError();
+  for (int b = 0; b < B; b += per) {
+    const unsigned total = (unsigned)((long long)(B - b < per ? B - b : per) * CG);
+    k<<<(total - 1) / 128 + 1, 128, 0, st>>>((const T*)x + b * ldx, ldx, w, bias,
+                                             (T*)s + (long long)b * (W - 1) * D,
+                                             (T*)y + (long long)b * D, D, CG, total);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess || B - b <= per) return e;
+  }
+  return cudaSuccess;
 }
 
 // The checks that all three calls share.

@@ -203,3 +203,30 @@ def test_ssm_long_memories():
         api.ssm_step(zero[0, :64], d[:, t], Ag, bc[0, :64], bc[0, :64], S, softplus=False)
     off = float(((S.double().log() - d.double().sum(1)[..., None] * Ag.double()) / n).mean())
     assert abs(off) < 0.5e-8, off
+
+
+def test_convolution_of_2_32_single_channels():
+    """More than 2^32 channels of one token, taken one by one (an odd channel
+    count): prompt and token are those of the same rows alone."""
+    _room(56)
+    B, D, W = (1 << 20) + 300, 4097, 2
+    assert B * D > 1 << 32
+    gen = torch.Generator(device="cuda").manual_seed(76)
+    x = torch.randn(B, D, generator=gen, device="cuda", dtype=torch.bfloat16)
+    s = torch.randn(B, 1, D, generator=gen, device="cuda", dtype=torch.bfloat16)
+    w, b = torch.randn(D, W, generator=gen, device="cuda"), torch.randn(D, device="cuda")
+    edge = ((1 << 32) - 256) // D  # sequences that 32 bits of threads count
+    some = [slice(0, 2), slice(edge - 2, edge + 2), slice(B - 2, B)]
+    n = torch.ones(B, dtype=torch.int32, device="cuda")
+    n[edge + 1] = n[1] = 0
+    y, sT = api.conv_fwd(x[:, None], w, b, s, lengths=n)
+    for i in some:
+        yi, si = api.conv_fwd(x[i, None].clone(), w, b, s[i].clone(), lengths=n[i].clone())
+        assert torch.equal(y[i], yi) and torch.equal(sT[i], si)
+    del y, sT
+    old = [s[i].clone() for i in some]
+    y = api.conv_step(x, w, s, b)
+    for i, o in zip(some, old):
+        assert torch.equal(y[i], api.conv_step(x[i].clone(), w, o, b))
+        assert torch.equal(s[i], o)
+    assert torch.equal(s[:, 0], x)
