@@ -369,6 +369,10 @@ conv_bwd_kernel(const T* __restrict__ x, long long ldx, const float* __restrict_
       back(dp, o);
       const int at = t - (W - 1);
       if (at < emit0 || at >= t1) continue;
+      if (at >= n) {  // no such token: zero, whatever the taps are
+#pragma unroll
+        for (int i = 0; i < P; ++i) o[i] = pack2(0.f, 0.f);
+      }
       const int r = t - n;  // row of the final state that holds input `at`
       if (gsb && r >= 0 && r < W - 1) {
         Row<T, V> rs;

@@ -230,3 +230,17 @@ def test_convolution_of_2_32_single_channels():
         assert torch.equal(y[i], api.conv_step(x[i].clone(), w, o, b))
         assert torch.equal(s[i], o)
     assert torch.equal(s[:, 0], x)
+
+
+BEHIND = [(20, 11), (20, 0), (9, 8), (300, 130)]  # T, tokens that exist
+
+
+@pytest.mark.parametrize("T,n", BEHIND)
+def test_conv_places_behind_the_last_token(T, n):
+    """Gradients of tokens that do not exist are zeros, whatever the taps."""
+    r = Rand(77)
+    x, gy, w = gpu(r.n(1, T, 12), r.n(1, T, 12), r.n(12, 4))
+    w[3, 0], w[5, 3], w[7, 1] = math.inf, math.nan, -math.inf
+    lens = torch.tensor([n], dtype=torch.int32, device="cuda")
+    got = api.conv_bwd(x, w, gy, lengths=lens)
+    assert not got["dx"][:, n:].any()
