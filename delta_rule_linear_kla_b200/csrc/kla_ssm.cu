@@ -729,7 +729,8 @@ bwd_kernel(BwdArgs q) {
         st4(ddt + (long long)t * p.D, vddt, m, vec);
         if (has_z) st4(dz + (long long)t * p.D, vdz, m, vec);
       }
-      // dB, dC: the warps' sums in order
+      // dB, dC: the warps' sums in order (for a token that does not exist they
+      // may be 0 times an infinite state)
       const float* bc = buf + 6 * Sh::XS + 2 * Sh::BS;
 #pragma unroll
       for (int i = 0; i < K * 2 * N / 4; i += NH) {
@@ -741,6 +742,7 @@ bwd_kernel(BwdArgs q) {
             const float4 a = *reinterpret_cast<const float4*>(bc + w * K * 2 * N + j);
             v.x += a.x; v.y += a.y; v.z += a.z; v.w += a.w;
           }
+          if (t0 + tt >= t_live) v = make_float4(0.f, 0.f, 0.f, 0.f);
           *reinterpret_cast<float4*>(pbc + (long long)(t0 + tt) * p.G * 2 * N + n) = v;
         }
       }

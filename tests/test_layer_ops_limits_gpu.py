@@ -244,3 +244,18 @@ def test_conv_places_behind_the_last_token(T, n):
     lens = torch.tensor([n], dtype=torch.int32, device="cuda")
     got = api.conv_bwd(x, w, gy, lengths=lens)
     assert not got["dx"][:, n:].any()
+
+
+@pytest.mark.parametrize("T,n", BEHIND)
+def test_ssm_places_behind_the_last_token(T, n):
+    """Gradients of tokens that do not exist are zeros, whatever the states,
+    their gradients and A."""
+    r = Rand(78)
+    B, D, N = 1, 12, 8
+    x, gy, dt, A, bc, gh, h0 = gpu(r.n(B, T, D), r.n(B, T, D), r.n(B, T, D), -torch.rand(D, N),
+                                   r.n(B, T, 1, N), r.n(B, D, N), r.n(B, D, N))
+    gh[0, 3, 2], gh[0, 5, 1], h0[0, 6, 3], A[7, 4] = math.inf, math.nan, -math.inf, math.nan
+    lens = torch.tensor([n], dtype=torch.int32, device="cuda")
+    got = api.ssm_bwd(x, dt, A, bc, bc, gy, z=x, h0=h0, grad_hT=gh, lengths=lens)
+    for k in ("du", "ddt", "dB", "dC", "dz"):
+        assert not got[k][:, n:].any(), k
