@@ -722,7 +722,7 @@ def conv_bwd_workspace_size(B: int, T: int, D: int, W: int) -> int:
 
 def _conv_args(x, w, bias, s0, lengths, lead, D, dt, dev):
     """The width, and the arguments x .. lengths of the C calls."""
-    if not isinstance(w, torch.Tensor) or w.dim() != 2 or w.shape[0] != D:
+    if not isinstance(w, torch.Tensor) or w.dim() != 2 or w.shape[0] != D or w.shape[1] < 1:
         raise ValueError("w must be a [D, W] CUDA tensor with D = %d" % D)
     W = w.shape[1]
     ldx = _rows(x, "x", dt, lead, (D,), dev)
@@ -921,6 +921,8 @@ def _qk_args(q, k, wq, wk, positions, inv_freq, norm, pos0):
     stride = rot = 0
     pp = pf = None
     if positions is not None:
+        if not isinstance(positions, torch.Tensor):
+            raise ValueError("positions must be a CUDA tensor")
         have = tuple(positions.shape)
         if have == lead:
             stride = T
@@ -931,6 +933,8 @@ def _qk_args(q, k, wq, wk, positions, inv_freq, norm, pos0):
     elif not -(1 << 31) <= pos0 <= (1 << 31) - max(T, 1):
         raise ValueError("positions from pos0 = %d on pass 32 bits" % pos0)
     if inv_freq is not None:
+        if not isinstance(inv_freq, torch.Tensor):
+            raise ValueError("inv_freq must be a CUDA tensor")
         rot = 2 * inv_freq.numel()
         pf = _p(inv_freq, "inv_freq", f32, inv_freq.shape, dev)
     return ty, dev, (B, T, Hq, Hk, d, rot), (

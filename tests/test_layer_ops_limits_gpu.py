@@ -259,3 +259,14 @@ def test_ssm_places_behind_the_last_token(T, n):
     got = api.ssm_bwd(x, dt, A, bc, bc, gy, z=x, h0=h0, grad_hT=gh, lengths=lens)
     for k in ("du", "ddt", "dB", "dC", "dz"):
         assert not got[k][:, n:].any(), k
+
+
+def test_arguments_that_are_no_tensors():
+    x = torch.zeros(2, 5, 64, device="cuda")
+    with pytest.raises(ValueError, match="w must be"):
+        api.conv_fwd(x, torch.zeros(64, 0, device="cuda"))
+    q = x.view(2, 5, 1, 64)
+    with pytest.raises(ValueError, match="positions must be a CUDA tensor"):
+        api.qk_norm_fwd(q, q, positions=[0, 1, 2, 3, 4])
+    with pytest.raises(ValueError, match="inv_freq must be a CUDA tensor"):
+        api.qk_norm_bwd(q, q, q, q, inv_freq=[1.0, 0.5])
