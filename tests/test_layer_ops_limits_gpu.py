@@ -1,4 +1,6 @@
-"""The layer operators at the ends of their arguments' ranges."""
+"""The layer operators at the ends of their arguments' ranges, and layouts and cuts
+beside the ones of test_layer_ops_gpu.py.  Bars are the ones of that file where
+none is derived here."""
 import math
 
 import pytest
@@ -7,7 +9,7 @@ import torch
 import delta_rule_linear_kla_b200 as K
 from delta_rule_linear_kla_b200 import api
 from oracle import layer_ops as ref
-from test_layer_ops_gpu import DT, Rand, U, check, gpu
+from test_layer_ops_gpu import DT, Rand, U, check, gpu, ssm_case, wide
 
 pytestmark = pytest.mark.gpu
 
@@ -270,3 +272,53 @@ def test_arguments_that_are_no_tensors():
         api.qk_norm_fwd(q, q, positions=[0, 1, 2, 3, 4])
     with pytest.raises(ValueError, match="inv_freq must be a CUDA tensor"):
         api.qk_norm_bwd(q, q, q, q, inv_freq=[1.0, 0.5])
+
+
+# B, T, D, G, N, dtype, z, skip, bias, softplus, state, lengths, -, columns before and behind u, dt
+WIDE = [
+    ((2, 70, 24, 1, 16, "bf16", True, True, True, True, True, [70, 33], 0), (8, 4), (4, 12)),
+    ((2, 41, 24, 2, 8, "fp32", True, True, True, True, True, None, 0), (4, 4), (3, 2)),
+    ((1, 67, 130, 1, 32, "bf16", False, True, True, True, False, None, 0), (5, 1), (1, 1)),
+    ((1, 33, 20, 1, 64, "fp32", True, False, True, True, True, [20], 0), (3, 2), (8, 0)),
+    ((1, 700, 64, 1, 16, "bf16", True, True, True, True, True, None, 0), (8, 8), (16, 0)),  # cut
+]
+
+
+@pytest.mark.parametrize("case,pu,pd", WIDE, ids=str)
+def test_ssm_rows_of_wider_matrices(case, pu, pd):
+    """u and dt as columns of wider matrices, NaN around them."""
+    _against_definition(case, lambda g: dict(g, u=wide(g["u"], *pu), dt=wide(g["dt"], *pd)))
+
+
+# cut into segments, with several blocks of channels a group and wide states
+CUT = [
+    (1, 700, 70, 1, 32, "fp32", True, True, True, True, True, None, 0),
+    (2, 600, 40, 1, 64, "bf16", True, True, True, True, True, [600, 290], 0),
+    (1, 520, 72, 2, 64, "fp32", False, True, True, True, False, None, 0),
+    (1, 530, 300, 1, 16, "bf16", True, True, True, True, True, [400], 0),
+    (1, 515, 270, 2, 8, "fp32", True, True, True, True, True, None, 0),
+]
+
+
+@pytest.mark.parametrize("case", CUT, ids=str)
+def test_ssm_cut_sequences(case):
+    B, T, D, G, N = case[:5]
+    assert api.ssm_fwd_workspace_size(B, T, D, G, N) > 0
+    _against_definition(case, lambda g: g)
+
+
+def _against_definition(case, lay):
+    a, gy, gh, n, c = ssm_case(case, 78)
+    g = lay({k: None if v is None else v.cuda() for k, v in a.items()})
+    kw = dict(softplus=case[9], lengths=None if n is None else n.cuda())
+    y, hT = api.ssm_fwd(**g, **kw)
+    want = ref.ssm(**a, softplus=case[9], lengths=case[11])
+    check(y, want["y"], c, "y")
+    check(hT, want["hT"], c, "hT")
+    got = api.ssm_bwd(g["u"], g["dt"], g["A"], g["Bm"], g["Cm"], gy.cuda(), g["D"], g["z"],
+                      g["dt_bias"], g["h0"], None if gh is None else gh.cuda(), **kw)
+    want = ref.ssm_bwd(a["u"], a["dt"], a["A"], a["Bm"], a["Cm"], gy, a["D"], a["z"],
+                       a["dt_bias"], a["h0"], gh, case[9], case[11])
+    for k, v in got.items():
+        if v is not None:
+            check(v, want[k], 2 * c + 128, k)
