@@ -19,8 +19,8 @@
 // 1e6 leaves 24-bit angles 0.06 off), their cosine and sine in fp32; norms
 // and products are fp32, and only the results are rounded, once.
 // Measured: 8 x 4096 tokens of 8 + 8 heads of 128, half of each turned, bf16:
-// 48 us, 5.5 TB/s of the 6.45 that a copy reaches.  Backward, 4 x 8192 tokens of
-// 32 + 8 heads of 64 with weights: 102 us, 5.0 TB/s.
+// 50 us, 5.4 TB/s of the 6.45 that a copy reaches.  Backward, 4 x 8192 tokens of
+// 32 + 8 heads of 64 with weights: 103 us, 4.9 TB/s.
 #include "kla_layer.cuh"
 
 namespace kla {

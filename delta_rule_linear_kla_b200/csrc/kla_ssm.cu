@@ -24,10 +24,10 @@
 // segments: their end states from zero starts in parallel (MODE LOCAL), a short
 // chain over segments, then all of them again from their true starts.
 //
-// Measured, 8 x 4096 x 2048 x 16 bf16: 440 us, where the exponentials alone
+// Measured, 8 x 4096 x 2048 x 16 bf16: 445 us, where the exponentials alone
 // take 235 and with the softplus and the gate 280.  Two blocks an SM keep the
-// special function unit 69 % busy over all SMs (256 blocks on 148), issue slots
-// 52 %, the shared-memory pipe 53 %: a mix in which moving work from one to
+// special function unit 68 % busy over all SMs (256 blocks on 148), issue slots
+// 51 %, the shared-memory pipe 48 %: a mix in which moving work from one to
 // another lost (operands stored twice, 464 us; B and C kept in bf16, 462; an
 // eighth or a quarter of the exponentials as polynomials, 464 and 481 when all
 // on the special function unit took 466).
@@ -504,7 +504,7 @@ chain_kernel(const float* __restrict__ A, const float* __restrict__ h0, float* e
 // registers and needs no selection.  What bounds it are issue slots (about 170
 // instructions a token for a thread's 8 states, 50 % of the slots used with two
 // recurrence warps a scheduler, which is what the registers allow).
-// 2 x 4096 x 2048 x 16 bf16: 375 us of the pass's 563.
+// 2 x 4096 x 2048 x 16 bf16: about 380 us of the pass's 575.
 // dB and dC leave as one part a channel tile, dA, dD and dt_bias as one a
 // segment, and reduce kernels add the parts in order: no atomics, the same
 // bits every time.
@@ -1086,7 +1086,7 @@ reduce_param_kernel(const float* __restrict__ pa, const float* __restrict__ pd, 
 //
 // Bound by HBM: one read and one write of the state.  A thread holds 4 states,
 // the N/4 threads of a channel lie side by side, and a block takes neighbouring
-// channels of one sequence (64 x 2048 x 16: 6.6 us; x 64 states: 22 us, 6.2 TB/s;
+// channels of one sequence (64 x 2048 x 16: 6.6 us, in 2.3 waves of blocks; x 64 states: 22 us, 6.2 TB/s;
 // two channels a thread: 6.5 and 23 us, and slower for a single sequence).
 template <typename T, int N>
 __global__ void __launch_bounds__(256)

@@ -488,7 +488,9 @@ KLA_API kla_status kla_conv_step(const void *x, long long ldx, const float *w, c
  * kla_ssm_bwd: every gradient for grad_y and grad_hT (nullable = 0); grad_D,
  * grad_dt_bias, grad_h0 nullable (not computed), grad_z needed with z.
  * Workspace kla_ssm_bwd_workspace_size(...): a state every 8 tokens
- * (B * T * D * N / 2 bytes) and parts of the sums over channels and tokens.
+ * (B * T * D * N / 2 bytes), dB and dC of every block of c channels of a group
+ * (8 * ceil(D / G / c) * B * T * G * N bytes, c = 64 for N <= 16, 32 for 32, 16
+ * for 64: then as much again as the states), and parts of the other sums.
  * kla_ssm_step: one token for each of B sequences (u, dt, z, y [B][D], Bm, Cm
  * [B][G][N]); state [B][D][N] fp32 moved on in place.
  */
@@ -524,7 +526,7 @@ KLA_API kla_status kla_ssm_step(const void *u, const void *dt, const float *A, c
  * 2.2; the rotation is that of arXiv 2104.09864, section 3.2).
  *
  *   norm 0: x^ = x;  1 (L2): x^ = x / sqrt(sum x^2 + eps);
- *   norm 2 (RMS): x^ = x / sqrt(sum x^2 / d + eps)
+ *   norm 2 (RMS): x^ = x / sqrt(sum x^2 / d + eps);  eps >= 0
  *   out = w x^, its first rot channels turned: pair i by the angle
  *   position * inv_freq[i], cosine and sine times scale; pairs are
  *   (i, i + rot/2), or (2i, 2i+1) when interleaved.
